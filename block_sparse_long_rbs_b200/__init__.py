@@ -17,12 +17,16 @@ import torch
 
 from ._abi import (  # noqa: F401
     DEVERR_BLOCK_INDEX,
+    DEVERR_LENGTH,
     DEVERR_NONCAUSAL,
+    DEVERR_PAGES,
     DEVERR_ROW_PTR,
+    DEVERR_SLOT,
     DEVERR_TIMEOUT,
     MAX_KV_BLOCKS,
     BlockListsC,
     Bf16Tensor,
+    KV4CacheC,
     RbsError,
     SelectParamsC,
     check,
@@ -33,7 +37,8 @@ __all__ = [
     "SelectParams", "BlockLists", "rbs_block_stats", "rbs_block_beta", "rbs_pool_queries", "rbs_select",
     "rbs_select_capacity", "rbs_select_workspace_bytes", "rbs_lists_causal_full", "rbs_lists_block_attention",
     "bsa_prefill", "bsa_prefill_rescue_weighted", "bsa_prefill_segments", "rope_reencode", "rbs_get_device_error",
-    "RbsError",
+    "rope_qk_norm", "KV4Cache", "rbs_kv4_page_bytes", "kv4_extend", "kv4_append", "kv4_load", "kv4_attend",
+    "rbs_kv4_attend_workspace_bytes", "RbsError",
 ]
 
 
@@ -342,6 +347,201 @@ def rope_reencode(x: torch.Tensor, old_pos: torch.Tensor, new_pos: torch.Tensor,
         check(lib().rope_reencode(ctypes.byref(tx), ctypes.byref(to), old_pos.data_ptr(), new_pos.data_ptr(), theta,
                                   rope_style, _stream()), "rope_reencode")
     return out
+
+
+# ---- serving: norm and rotation, the 4-bit cache ----------------------------
+# These run once per layer and decoding step, where the call itself counts:
+# the current device is switched only when it is another one, and the stream
+# is taken as a raw handle.
+
+
+def _call(dev: torch.device, fn, where: str, *args) -> None:
+    """fn(*args, stream) on dev's current stream."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        check(st, where)
+
+
+def _ints(x, name: str, dev: torch.device, *shape: int) -> int:
+    """Device pointer of a contiguous int32 tensor of the given shape on dev."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if x.dtype != torch.int32 or not x.is_contiguous():
+        raise TypeError(f"{name}: expected a contiguous int32 CUDA tensor")
+    if tuple(x.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(x.shape)}")
+    if x.device != dev:
+        raise ValueError(f"{name} is on {x.device}, expected {dev}: every tensor of a call must be on one device")
+    return x.data_ptr()
+
+
+def _table(x, name: str, dev: torch.device, rows: int) -> tuple[int, int, int]:
+    """Pointer, row stride and width of an int32 [rows, width] table with contiguous rows on dev."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if x.dtype != torch.int32 or x.dim() != 2 or x.stride(1) != 1:
+        raise TypeError(f"{name}: expected an int32 CUDA tensor [batch, max_pages] with contiguous rows")
+    if x.shape[0] != rows:
+        raise ValueError(f"{name}: expected {rows} rows, got {x.shape[0]}")
+    if x.device != dev:
+        raise ValueError(f"{name} is on {x.device}, expected {dev}: every tensor of a call must be on one device")
+    return x.data_ptr(), max(x.stride(0), x.shape[1]) if rows == 1 else x.stride(0), x.shape[1]
+
+
+def rope_qk_norm(Q: torch.Tensor, K: torch.Tensor, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+                 pos: torch.Tensor, theta: float, eps: float = 1e-6, rope_style: int = 0,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """Per-head norm of queries and keys and their rotation to pos ([L] or [B, L] int32), one pass.
+    Returns (q_out, k_out); an output may be its input, for in place."""
+    if q_out is None:
+        q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    if k_out is None:
+        k_out = torch.empty(K.shape, dtype=K.dtype, device=K.device)
+    tq, tk, to, tp = _t(Q, "Q"), _t(K, "K"), _t(q_out, "q_out"), _t(k_out, "k_out")
+    dev = Q.device
+    if K.device != dev or q_out.device != dev or k_out.device != dev:
+        _one_device("Q", Q, K=K, q_out=q_out, k_out=k_out)
+    B, L = Q.shape[:2]
+    shared = isinstance(pos, torch.Tensor) and pos.dim() == 1
+    p_ptr = _ints(pos, "pos", dev, L) if shared else _ints(pos, "pos", dev, B, L)
+    w = []
+    for x, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if x is not None:
+            if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 1 or not x.is_contiguous():
+                raise TypeError(f"{name}: expected a contiguous bfloat16 CUDA tensor [128]")
+            if x.shape[0] != Q.shape[3]:
+                raise ValueError(f"{name}: expected {Q.shape[3]} weights, got {x.shape[0]}")
+            if x.device != dev:
+                _one_device("Q", Q, **{name: x})
+        w.append(None if x is None else x.data_ptr())
+    _call(dev, lib().rope_qk_norm, "rope_qk_norm", tq, to, tk, tp, w[0], w[1], eps, p_ptr, 0 if shared else L, theta,
+          rope_style)
+    return q_out, k_out
+
+
+def rbs_kv4_page_bytes(page_size: int) -> int:
+    """Bytes of one page of one KV head of the 4-bit cache."""
+    n = int(lib().rbs_kv4_page_bytes(page_size))
+    if n < 0:
+        raise RbsError(2, "rbs_kv4_page_bytes", lib().rbs_last_error().decode())
+    return n
+
+
+@dataclasses.dataclass
+class KV4Cache:
+    """A paged key/value cache in 4 bits (format and layout in include/rbs.h)."""
+
+    data: torch.Tensor  # uint8 [num_pages, Hkv, rbs_kv4_page_bytes(page_size)]
+    page_size: int
+    k_scale: float = 1.0  # powers of two that the stored scales are relative to
+    v_scale: float = 1.0
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int, kv_heads: int, device="cuda", k_scale: float = 1.0,
+              v_scale: float = 1.0) -> "KV4Cache":
+        return KV4Cache(torch.empty(num_pages, kv_heads, rbs_kv4_page_bytes(page_size), dtype=torch.uint8,
+                                    device=device), page_size, k_scale, v_scale)
+
+    def c(self) -> KV4CacheC:
+        x = self.data
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("cache.data: expected a torch.Tensor")
+        if not x.is_cuda or x.dtype != torch.uint8 or not x.is_contiguous() or x.dim() != 3:
+            raise TypeError("cache.data: expected a contiguous uint8 CUDA tensor [num_pages, Hkv, page bytes]")
+        # a page is page_size / 16 sub-blocks of 2304 bytes; the library checks the page size itself
+        if x.shape[2] != self.page_size // 16 * 2304:
+            raise ValueError(f"cache.data: pages of {x.shape[2]} bytes, expected {self.page_size // 16 * 2304}")
+        return KV4CacheC(x.data_ptr(), x.shape[0], x.shape[1], self.page_size, self.k_scale, self.v_scale)
+
+
+def kv4_extend(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+               free_head: torch.Tensor, max_new: int, page_size: int, slots: torch.Tensor | None = None,
+               pos: torch.Tensor | None = None, free_head_out: torch.Tensor | None = None):
+    """Pages from the free list for requests that grow from old_lens to new_lens ([B] int32): updates block_table
+    [B, max_pages] in place and returns (slots, pos, free_head_out), the slots and positions [B, max_new] of the new
+    tokens (-1 past a request's last one) and the count of free pages taken so far."""
+    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
+        raise TypeError("block_table: expected a CUDA tensor")
+    dev, B = block_table.device, block_table.shape[0]
+    t_ptr, stride, width = _table(block_table, "block_table", dev, B)
+    if max_new < 0:
+        raise ValueError("max_new must be positive")
+    if slots is None:
+        slots = torch.empty(B, max_new, dtype=torch.int32, device=dev)
+    if pos is None:
+        pos = torch.empty(B, max_new, dtype=torch.int32, device=dev)
+    if free_head_out is None:
+        free_head_out = torch.empty(1, dtype=torch.int32, device=dev)
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise TypeError("free_pages: expected a contiguous int32 CUDA tensor [num_free]")
+    n = free_pages.shape[0]
+    _call(dev, lib().kv4_extend, "kv4_extend", t_ptr, stride, B, width, _ints(old_lens, "old_lens", dev, B),
+          _ints(new_lens, "new_lens", dev, B), _ints(free_pages, "free_pages", dev, n), n,
+          _ints(free_head, "free_head", dev, 1), page_size, max_new, _ints(slots, "slots", dev, B, max_new),
+          _ints(pos, "pos", dev, B, max_new), _ints(free_head_out, "free_head_out", dev, 1))
+    return slots, pos, free_head_out
+
+
+def kv4_append(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor) -> None:
+    """Quantise K and V [B, L, Hkv, 128] into the cache's slots [B, L] (int32; negative: padding, skipped)."""
+    tk, tv, c = _t(K, "K"), _t(V, "V"), cache.c()
+    dev = K.device
+    if V.device != dev or cache.data.device != dev:
+        _one_device("K", K, V=V, cache=cache.data)
+    _call(dev, lib().kv4_append, "kv4_append", c, tk, tv, _ints(slots, "slots", dev, K.shape[0], K.shape[1]))
+
+
+def kv4_load(cache: KV4Cache, slots: torch.Tensor, k_out: torch.Tensor | None = None,
+             v_out: torch.Tensor | None = None):
+    """The cached keys and values of slots [B, L] as bf16 [B, L, Hkv, 128] (zeros for negative slots)."""
+    c = cache.c()
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+        raise TypeError("slots: expected a contiguous int32 CUDA tensor [B, L]")
+    dev, shape = cache.data.device, (slots.shape[0], slots.shape[1], cache.data.shape[1], 128)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    tk, tv = _t(k_out, "k_out"), _t(v_out, "v_out")
+    if k_out.device != dev or v_out.device != dev:
+        _one_device("cache", cache.data, k_out=k_out, v_out=v_out)
+    _call(dev, lib().kv4_load, "kv4_load", c, _ints(slots, "slots", dev, k_out.shape[0], k_out.shape[1]), tk, tv)
+    return k_out, v_out
+
+
+def rbs_kv4_attend_workspace_bytes(seqlen_q: int, heads_q: int, kv_heads: int) -> int:
+    return int(lib().rbs_kv4_attend_workspace_bytes(seqlen_q, heads_q, kv_heads))
+
+
+def kv4_attend(Q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, lens: torch.Tensor,
+               starts: torch.Tensor | None = None, window: int = 0, sinks: int = 0,
+               softmax_scale: float | None = None, out: torch.Tensor | None = None, return_lse: bool = False,
+               workspace: torch.Tensor | None = None):
+    """Attention of new tokens Q [B, Lq, Hq, 128] over the cached keys and values of their requests: query t of
+    request b is at position starts[b] + t (lens[b] - Lq + t without starts) and sees the keys up to its own, with
+    window > 0 only the last `window` of them and the first `sinks`."""
+    tq, c = _t(Q, "Q"), cache.c()
+    dev = Q.device
+    B, Lq, Hq, D = Q.shape
+    if out is None:
+        out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+    lse = torch.empty(B, Hq, Lq, dtype=torch.float32, device=dev) if return_lse else None
+    if workspace is None:
+        workspace = torch.empty(rbs_kv4_attend_workspace_bytes(Lq, Hq, cache.data.shape[1]), dtype=torch.uint8,
+                                device=dev)
+    to, w_ptr = _t(out, "out"), _dev(workspace, "workspace", torch.uint8)
+    if cache.data.device != dev or out.device != dev or workspace.device != dev:
+        _one_device("Q", Q, cache=cache.data, out=out, workspace=workspace)
+    t_ptr, stride, width = _table(block_table, "block_table", dev, B)
+    _call(dev, lib().kv4_attend, "kv4_attend", tq, c, t_ptr, stride, width, _ints(lens, "lens", dev, B),
+          None if starts is None else _ints(starts, "starts", dev, B), window, sinks,
+          1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale, w_ptr, workspace.numel(), to,
+          None if lse is None else lse.data_ptr())
+    return (out, lse) if return_lse else out
 
 
 def rbs_get_device_error() -> int:

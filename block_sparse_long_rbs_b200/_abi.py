@@ -16,6 +16,7 @@ RBS_OK = 0
 STATUS_NAMES = {0: "RBS_OK", 1: "RBS_ERR_INVALID_ARG", 2: "RBS_ERR_UNSUPPORTED", 3: "RBS_ERR_CAPACITY",
                 4: "RBS_ERR_CUDA", 5: "RBS_ERR_DEVICE"}
 DEVERR_BLOCK_INDEX, DEVERR_ROW_PTR, DEVERR_TIMEOUT, DEVERR_NONCAUSAL = 0x1, 0x2, 0x4, 0x8
+DEVERR_SLOT, DEVERR_LENGTH, DEVERR_PAGES = 0x10, 0x20, 0x40
 MAX_SEGMENTS = 512
 MAX_KV_BLOCKS = 4096
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -39,6 +40,11 @@ class SelectParamsC(ctypes.Structure):
 class BlockListsC(ctypes.Structure):
     _fields_ = [("row_ptr", ctypes.c_void_p), ("col_idx", ctypes.c_void_p), ("flags", ctypes.c_void_p),
                 ("capacity", ctypes.c_int64), ("num_rows", ctypes.c_int32)]
+
+
+class KV4CacheC(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
 P = ctypes.POINTER
@@ -70,6 +76,15 @@ SIGNATURES = {
     "bsa_prefill_segments": (ctypes.c_int, [P(Bf16Tensor), P(Bf16Tensor), P(Bf16Tensor), P(BlockListsC), i32, i32,
                                             i64, P(i32), i32, i32, f32, P(Bf16Tensor), vp, vp]),
     "rope_reencode": (ctypes.c_int, [P(Bf16Tensor), P(Bf16Tensor), vp, vp, f32, i32, vp]),
+    "rope_qk_norm": (ctypes.c_int, [P(Bf16Tensor), P(Bf16Tensor), P(Bf16Tensor), P(Bf16Tensor), vp, vp, f32, vp, i64,
+                                    f32, i32, vp]),
+    "rbs_kv4_page_bytes": (i64, [i32]),
+    "kv4_extend": (ctypes.c_int, [vp, i64, i32, i32, vp, vp, vp, i64, vp, i32, i32, vp, vp, vp, vp]),
+    "kv4_append": (ctypes.c_int, [P(KV4CacheC), P(Bf16Tensor), P(Bf16Tensor), vp, vp]),
+    "kv4_load": (ctypes.c_int, [P(KV4CacheC), vp, P(Bf16Tensor), P(Bf16Tensor), vp]),
+    "rbs_kv4_attend_workspace_bytes": (sz, [i64, i64, i64]),
+    "kv4_attend": (ctypes.c_int, [P(Bf16Tensor), P(KV4CacheC), vp, i64, i32, vp, vp, i32, i32, f32, vp, sz,
+                                  P(Bf16Tensor), vp, vp]),
     "rbs_testing_bsa_prefill_stalled": (ctypes.c_int, [P(Bf16Tensor), P(Bf16Tensor), P(Bf16Tensor), P(BlockListsC),
                                                        i32, i32, ctypes.c_uint64, i32, P(Bf16Tensor), vp]),
     "rbs_testing_exp2": (ctypes.c_int, [vp, vp, i64, vp]),

@@ -1,0 +1,589 @@
+// Attention of new tokens over the 4-bit paged cache.
+//
+// For query t of request b at position p = start_b + t and q head h of KV
+// head h / G:
+//   O = sum_s softmax_s(scale q . k_s) v_s  over the cached keys s <= p,
+// with a window W also p - W < s or s < S (the S first tokens stay visible).
+//
+// A work item is (request, KV head, tile of 8 NT query rows), rows being the
+// (token, q head of the group) pairs that share the KV head, so a cached byte
+// is read once for all of them.  An item's visible sub-blocks (16 tokens)
+// form units of eight, one per warp; all items' units in one sequence are cut
+// into equal runs, one per CTA, so unequal lengths leave no CTA idle.  An item
+// that a CTA holds whole is finished there; parts of items split between CTAs
+// go to the workspace as (max, sum, unnormalised output) and
+// kv4_combine_kernel joins them in their order, so results do not vary.
+//
+// A warp works on its own sub-blocks with no barrier: 2304 bytes by 16-byte
+// asynchronous copies into its ring, then
+//   S^T (16 keys x 8 rows) = K Q^T,  O^T (16 dims x 8 rows) += V^T P^T
+// by mma.m16n8k16 in fp16 with fp32 sums: rows of queries are the instruction's
+// narrow side, since one token's G rows rarely fill the wide one.  The codes
+// become fp16 by the e2m1 conversion, and times their scale stay exact; Q is
+// brought to fp16 by a power of two per row (bf16's 8 bits fit fp16's 11; values
+// more than 2^26 below the row's largest lose bits that fp32 sums would lose as
+// well); P = 2^6 exp2(s - m) is rounded to fp16 once (2^-12 relative), m at most
+// 2^8 below the running maximum, so that an update is rare; keys down to 2^-31
+// of the largest still count.  Sums and outputs stay in fp32.
+// Keys that no row may see get the value scale 0 (their bytes may be
+// anything, NaN scales too); a sub-block that some rows see only in part is
+// taken once per query token, for that token's rows alone and with the keys it
+// may not see set to zero.
+// Bound by memory: 144 bytes per cached token and KV head.
+#pragma once
+
+#include <type_traits>
+
+#include "kv4.cuh"
+
+namespace rbs {
+
+constexpr int kAttWarps = 8;
+constexpr int kAttThreads = kAttWarps * 32;
+constexpr int kAttStages = 4;
+constexpr int kAttMaxBatch = 4096;
+constexpr float kAttPShift = 6.f;  // P carries 2^6
+
+struct Kv4AttArgs {
+  const uint8_t* data;
+  int64_t num_pages;
+  int Hkv, G, page, spp;      // spp: sub-blocks per page
+  uint32_t spp_magic;         // ceil(2^32 / spp); 0 when spp is 1
+  const int32_t* table;
+  int64_t table_b;
+  int max_pages, B, Lq;
+  const int32_t *lens, *starts;
+  int window, sinks;
+  const __nv_bfloat16* q;
+  int64_t qb, qs, qh;
+  __nv_bfloat16* o;
+  int64_t ob, os, oh;
+  float* lse;  // [B, Hq, Lq] or null
+  float scale_log2;  // softmax scale * log2(e) * k_scale
+  float v_scale;
+  int tiles;  // row tiles of 8 NT rows per (request, KV head)
+  float *part_o, *part_ml;  // workspace: two slots per CTA
+  int ctas;  // CTAs of the main kernel
+};
+
+// A request's visible range for its queries: sub-blocks [0, sink) and
+// [lo, hi), and the positions of its queries.
+struct AttRange {
+  int first_q, len, sink, lo, n;  // n: sub-blocks in all
+};
+
+__device__ __forceinline__ AttRange att_range(const Kv4AttArgs& a, int b) {
+  AttRange r;
+  const int64_t most = static_cast<int64_t>(a.max_pages) * a.page;
+  r.len = static_cast<int>(min(static_cast<int64_t>(max(__ldg(a.lens + b), 0)), most));
+  r.first_q = a.starts != nullptr ? __ldg(a.starts + b) : r.len - a.Lq;
+  const int64_t qmin = max(r.first_q, 0);
+  const int64_t qmax = min(static_cast<int64_t>(r.first_q) + a.Lq, static_cast<int64_t>(r.len)) - 1;
+  r.sink = r.lo = r.n = 0;
+  if (qmax < qmin) return r;
+  if (a.window > 0) {
+    r.lo = static_cast<int>(max(qmin - a.window + 1, static_cast<int64_t>(0)) >> 4);
+    r.sink = static_cast<int>(min((static_cast<int64_t>(a.sinks) + 15) >> 4, static_cast<int64_t>(r.lo)));
+  }
+  r.n = r.sink + static_cast<int>(qmax >> 4) + 1 - r.lo;
+  return r;
+}
+
+// Prefix sums of the requests' units into shared memory, prefix[B] their sum.
+// A request with nothing visible has one unit, which writes its empty rows.
+__device__ __forceinline__ void att_units(const Kv4AttArgs& a, int32_t* prefix, int64_t* sums) {
+  int64_t carry = 0;
+  for (int base = 0; base < a.B; base += blockDim.x) {
+    const int b = base + threadIdx.x;
+    int64_t v = 0;
+    if (b < a.B) v = max(1, (att_range(a, b).n + kAttWarps - 1) / kAttWarps);
+    int64_t total;
+    const int64_t before = block_exclusive_scan(v, sums, total);
+    if (b < a.B) prefix[b] = static_cast<int32_t>(carry + before);
+    carry += total;
+  }
+  if (threadIdx.x == 0) prefix[a.B] = static_cast<int32_t>(carry);
+  __syncthreads();
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// Four e2m1 pairs (a word) as f16x2 each.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+// Four e4m3 scales (a word) as two f16x2.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, x, 0x1010); }
+__device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, x, 0x3232); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
+  return v;
+}
+
+template <int NT>
+struct AttSmem {
+  static constexpr int kRing = 0;
+  static constexpr int kQ = kRing + kAttWarps * kAttStages * kSubBytes;  // Q fragments [8 groups][NT][32 lanes][8 B]
+  static constexpr int kQExp = kQ + 8 * NT * 256;                        // float [8 NT]: the rows' powers of two
+  static constexpr int kMerge = kQExp + 8 * NT * 4;                      // float [8 warps][8 rows][128 + 4]
+  static constexpr int kML = kMerge + kAttWarps * 8 * 132 * 4;           // float [8 warps][8 NT][2]
+  static constexpr int kSums = kML + kAttWarps * 8 * NT * 8;             // int64 [warps]
+  static constexpr int kPrefix = kSums + kAttWarps * 8;                  // int32 [B + 1]
+  static constexpr int bytes(int B) { return kPrefix + (B + 1) * 4; }
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kernel(const __grid_constant__ Kv4AttArgs a) {
+  using L = AttSmem<NT>;
+  constexpr int R = 8 * NT;  // rows of a tile
+  extern __shared__ __align__(16) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  float* qexp = reinterpret_cast<float*>(smem + L::kQExp);
+  float* merge = reinterpret_cast<float*>(smem + L::kMerge);
+  float* ml = reinterpret_cast<float*>(smem + L::kML);
+  int64_t* sums = reinterpret_cast<int64_t*>(smem + L::kSums);
+  int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefix);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, j = lane & 3;
+  const uint32_t ring = sb + L::kRing + warp * kAttStages * kSubBytes;
+
+  att_units(a, prefix, sums);
+  if (blockIdx.x == 0)
+    for (int b = tid; b < a.B; b += kAttThreads) {
+      const int len = __ldg(a.lens + b);
+      if (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.page) raise_error(RBS_DEVERR_LENGTH);
+    }
+  const int HT = a.Hkv * a.tiles;
+  const int64_t total = static_cast<int64_t>(prefix[a.B]) * HT;
+  int64_t u = total * blockIdx.x / a.ctas;
+  const int64_t u_end = total * (blockIdx.x + 1) / a.ctas;
+  bool first_part = true;
+
+  while (u < u_end) {
+    // the item of unit u: request (last b with prefix[b] HT <= u), KV head, row tile
+    int lo_b = 0, hi_b = a.B - 1;
+    const int64_t target = u / HT;
+    while (lo_b < hi_b) {
+      const int mid = (lo_b + hi_b + 1) >> 1;
+      if (prefix[mid] <= target) lo_b = mid; else hi_b = mid - 1;
+    }
+    const int b = lo_b, nu = prefix[b + 1] - prefix[b];
+    const int64_t rem = u - static_cast<int64_t>(prefix[b]) * HT;
+    const int ht = static_cast<int>(rem / nu);
+    const int ua = static_cast<int>(rem - static_cast<int64_t>(ht) * nu);
+    const int ub = static_cast<int>(min(static_cast<int64_t>(nu), ua + (u_end - u)));
+    const int kvh = ht / a.tiles, tile = ht - kvh * a.tiles;
+    u += ub - ua;
+    const AttRange rg = att_range(a, b);
+    const int rows = a.G * a.Lq, row0 = tile * R;
+
+    // ---- Q fragments: row n of the tile, dims 16 s + {2j, 2j + 1, 2j + 8, 2j + 9}
+    __syncthreads();  // the previous item's readers are done
+    for (int n = warp; n < R; n += kAttWarps) {
+      const int row = row0 + n;
+      uint2 x = make_uint2(0, 0);
+      if (row < rows) {
+        const int t = row / a.G, g = row - t * a.G;
+        x = *reinterpret_cast<const uint2*>(a.q + b * a.qb + t * a.qs + (kvh * a.G + g) * a.qh + 4 * lane);
+      }
+      const float v[4] = {bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y)};
+      float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      // the row times 2^-e, its largest in [2^11, 2^12); e kept in the range where 2^e and 2^-e are normal
+      const int e = (m > 0.f && m < INFINITY) ? max(-126, min(126, static_cast<int>(__float_as_uint(m) >> 23) - 127 - 11)) : 0;
+      const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      // lane holds dims 4 lane .. 4 lane + 3 of group s = lane / 4: k = 4 (lane % 4) ..
+      const int s = lane >> 2, k0 = 4 * (lane & 3);
+      const uint32_t w0 = pack_f16x2(v[0] * up, v[1] * up), w1 = pack_f16x2(v[2] * up, v[3] * up);
+      const uint32_t dst = sb + L::kQ + ((s * NT + (n >> 3)) * 32 + (n & 7) * 4) * 8;
+      // pair k, k + 1 belongs to lane (n % 8, (k % 8) / 2), word k / 8
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + ((k0 & 7) >> 1) * 8 + (k0 >> 3) * 4), "r"(w0) : "memory");
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (((k0 + 2) & 7) >> 1) * 8 + (k0 >> 3) * 4), "r"(w1) : "memory");
+      if (lane == 0) qexp[n] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    }
+    __syncthreads();
+
+    // ---- this thread's columns of S^T: rows 8 nt + 2j + {0, 1}
+    float sc[NT][2];
+    int qp[NT][2];
+    float m_run[NT][2], l_run[NT][2], o[8][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int n = 8 * nt + 2 * j + i, row = row0 + n;
+        sc[nt][i] = a.scale_log2 * qexp[n];
+        const int p = row < rows ? rg.first_q + row / a.G : -1;
+        qp[nt][i] = p < rg.len ? p : -1;  // -1: the row sees nothing
+        m_run[nt][i] = -INFINITY;
+        l_run[nt][i] = 0.f;
+      }
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[s][nt][q] = 0.f;
+    // positions of the tile's queries: [p_lo, p_hi], and whether all of them exist
+    const int t_lo = row0 / a.G, t_hi = (min(row0 + R, rows) - 1) / a.G;
+    const int p_lo = rg.first_q + t_lo, p_hi = rg.first_q + t_hi;
+    const bool all_live = p_lo >= 0 && p_hi < rg.len;
+
+    // ---- sub-blocks v = 8 k + warp of units [ua, ub)
+    const int v_end = min(ub * kAttWarps, rg.n);
+    int v_load = ua * kAttWarps + warp;
+    auto real_sub = [&](int v) { return v < rg.sink ? v : v - rg.sink + rg.lo; };
+    auto page_of = [&](int sub) {
+      return a.spp_magic != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(sub), a.spp_magic)) : sub;
+    };
+    auto entry = [&](int v) -> int {
+      return v < v_end ? __ldg(a.table + b * a.table_b + page_of(real_sub(v))) : 0;
+    };
+    uint32_t taken = 0;  // bit per stage issued, newest lowest: its page was valid
+    int pg_next = entry(v_load);
+    int issued = 0;
+    auto issue = [&]() {
+      const bool any = v_load < v_end;
+      const bool ok = any && pg_next >= 0 && pg_next < a.num_pages;
+      if (any && !ok && lane == 0) raise_error(RBS_DEVERR_BLOCK_INDEX);
+      if (any) {
+        const int sub = real_sub(v_load), pgi = page_of(sub);
+        const uint8_t* src = a.data + ((static_cast<int64_t>(ok ? pg_next : 0) * a.Hkv + kvh) * a.spp + (sub - pgi * a.spp)) * kSubBytes;
+        const uint32_t dst = ring + (issued % kAttStages) * kSubBytes;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) cp_async16(dst + 512 * q + 16 * lane, src + 512 * q + 16 * lane, ok);
+        if (lane < 16) cp_async16(dst + 2048 + 16 * lane, src + 2048 + 16 * lane, ok);
+      }
+      cp_async_commit();
+      taken = (taken << 1) | (ok ? 1u : 0u);
+      ++issued;
+      v_load += kAttWarps;
+      pg_next = entry(v_load);
+    };
+#pragma unroll
+    for (int q = 0; q < kAttStages - 1; ++q) issue();
+
+    int done = 0;
+    for (int v = ua * kAttWarps + warp; v < v_end; v += kAttWarps, ++done) {
+      cp_async_wait<kAttStages - 2>();
+      __syncwarp();  // every lane's copies have landed, and the stage issued next is read out
+      issue();
+      const uint32_t st = ring + (done % kAttStages) * kSubBytes;
+      const bool valid = (taken >> (kAttStages - 1)) & 1u;
+      const int tok0 = real_sub(v) * 16;
+      // fully visible to every row of the tile
+      const bool full = valid && all_live && tok0 + 15 <= p_lo &&
+                        (a.window == 0 || tok0 > p_hi - a.window || tok0 + 15 < a.sinks);
+      // ---- S^T = K Q^T
+      const uint4 ka = lds128(st + 16 * lane), kb = lds128(st + 512 + 16 * lane);
+      const uint2 sa = lds64(st + 2048 + 8 * r), sbk = lds64(st + 2048 + 64 + 8 * r);
+      float c[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[nt][q] = 0.f;
+      {
+        uint32_t fa[4], fb[4];  // f16x2 scales of groups (0,1), (2,3), ...
+        e4m3x4_f16(sa.x, fa[0], fa[1]);
+        e4m3x4_f16(sa.y, fa[2], fa[3]);
+        e4m3x4_f16(sbk.x, fb[0], fb[1]);
+        e4m3x4_f16(sbk.y, fb[2], fb[3]);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t xa[4], xb[4];
+          e2m1x8_f16(wa[w], xa);
+          e2m1x8_f16(wb[w], xb);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int s = 2 * w + e;
+            const uint32_t ga = e == 0 ? dup_lo(fa[w]) : dup_hi(fa[w]), gb = e == 0 ? dup_lo(fb[w]) : dup_hi(fb[w]);
+            const uint32_t a0 = hmul2(xa[2 * e], ga), a1 = hmul2(xb[2 * e], gb);
+            const uint32_t a2 = hmul2(xa[2 * e + 1], ga), a3 = hmul2(xb[2 * e + 1], gb);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 qf = lds64(sb + L::kQ + ((s * NT + nt) * 32 + lane) * 8);
+              mma_f16(c[nt], a0, a1, a2, a3, qf.x, qf.y);
+            }
+          }
+        }
+      }
+      // ---- scores in log2 units, masked; c[nt][2 i + q]: key r + 8 i, row column q
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[nt][q] *= sc[nt][q & 1];
+      if (!full) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = tok0 + r + 8 * (q >> 1), p = qp[nt][q & 1];
+            const bool see = valid && key <= p && (a.window == 0 || key > p - a.window || key < a.sinks);
+            if (!see) c[nt][q] = -INFINITY;
+          }
+      }
+      // ---- running maximum, moved only when a score passes it by 2^8
+      bool up = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) up = up || fmaxf(c[nt][i], c[nt][2 + i]) > m_run[nt][i] + 8.f;
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = fmaxf(c[nt][i], c[nt][2 + i]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m_run[nt][i], mx);
+            const float f = m_run[nt][i] == -INFINITY ? 0.f : ptx_exp2(m_run[nt][i] - mn);
+            m_run[nt][i] = mn;
+            l_run[nt][i] *= f;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+              o[s][nt][i] *= f;
+              o[s][nt][2 + i] *= f;
+            }
+          }
+      }
+      // ---- P^T as the second product's operand: keys 2j, 2j + 1 (+ 8) of row r
+      uint32_t p0[NT], p1[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float m = m_run[nt][q & 1] == -INFINITY ? 0.f : m_run[nt][q & 1];
+          e[q] = ptx_exp2(c[nt][q] - m + kAttPShift);
+        }
+        l_run[nt][0] += e[0] + e[2];
+        l_run[nt][1] += e[1] + e[3];
+        p0[nt] = movmatrix_trans(pack_f16x2(e[0], e[1]));
+        p1[nt] = movmatrix_trans(pack_f16x2(e[2], e[3]));
+      }
+      // ---- O^T += V^T P^T; group s is dims 16 s .. 16 s + 15 of the instruction's 16 rows
+      const uint4 va = lds128(st + 1024 + 16 * lane), vb = lds128(st + 1536 + 16 * lane);
+      const uint4 ta = lds128(st + 2176 + 16 * j), tb = lds128(st + 2176 + 64 + 16 * j);
+      // all columns, or (part) the columns of token t alone: 0 times a NaN
+      // value is one, so other columns are left out and not given zero weights
+      auto product = [&](auto part, uint32_t keep_a, uint32_t keep_b, int t) {
+        bool mine[NT][2];
+        if (part)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) mine[nt][i] = (row0 + 8 * nt + 2 * j + i) / a.G == t;
+        const uint32_t ya[4] = {ta.x & keep_a, ta.y & keep_a, ta.z & keep_a, ta.w & keep_a};
+        const uint32_t yb[4] = {tb.x & keep_b, tb.y & keep_b, tb.z & keep_b, tb.w & keep_b};
+#pragma unroll
+        for (int hw = 0; hw < 2; ++hw) {  // groups 4 hw .. 4 hw + 3
+          const uint32_t a_0 = hw ? va.y : va.x, a_1 = hw ? va.w : va.z;  // keys 2j, 2j + 1
+          const uint32_t b_0 = hw ? vb.y : vb.x, b_1 = hw ? vb.w : vb.z;  // keys 2j + 8, 2j + 9
+          uint32_t xl[4], xh[4], zl[4], zh[4];
+          constexpr uint32_t k = 0x0f0f0f0fu;
+          e2m1x8_f16((a_0 & k) | ((a_1 << 4) & ~k), xl);  // dim r of both keys
+          e2m1x8_f16(((a_0 >> 4) & k) | (a_1 & ~k), xh);  // dim r + 8
+          e2m1x8_f16((b_0 & k) | ((b_1 << 4) & ~k), zl);
+          e2m1x8_f16(((b_0 >> 4) & k) | (b_1 & ~k), zh);
+          uint32_t ga[4], gb[4];
+          e4m3x4_f16(ya[2 * hw], ga[0], ga[1]);
+          e4m3x4_f16(ya[2 * hw + 1], ga[2], ga[3]);
+          e4m3x4_f16(yb[2 * hw], gb[0], gb[1]);
+          e4m3x4_f16(yb[2 * hw + 1], gb[2], gb[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a0 = hmul2(xl[e], ga[e]), a1 = hmul2(xh[e], ga[e]);
+            const uint32_t a2 = hmul2(zl[e], gb[e]), a3 = hmul2(zh[e], gb[e]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (part) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(d, a0, a1, a2, a3, p0[nt], p1[nt]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  if (mine[nt][q & 1]) o[4 * hw + e][nt][q] += d[q];
+              } else {
+                mma_f16(o[4 * hw + e][nt], a0, a1, a2, a3, p0[nt], p1[nt]);
+              }
+            }
+          }
+        }
+      };
+      if (full) {
+        product(std::false_type{}, 0xffffffffu, 0xffffffffu, 0);
+      } else {
+        // once per query token, with the keys it sees
+        for (int t = t_lo; t <= t_hi; ++t) {
+          const int pt = rg.first_q + t;
+          auto keep = [&](int k0) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int key = tok0 + k0 + i;
+              if (valid && pt < rg.len && key <= pt && (a.window == 0 || key > pt - a.window || key < a.sinks))
+                m |= 0x00ff00ffu << (8 * i);
+            }
+            return m;
+          };
+          product(std::true_type{}, keep(2 * j), keep(2 * j + 8), t);
+        }
+      }
+    }
+    cp_async_wait<0>();
+
+    // ---- join the warps: row sums over lanes, then every row over the warps
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float l = l_run[nt][i];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (r == 0) {
+          const int n = 8 * nt + 2 * j + i;
+          ml[(warp * R + n) * 2] = m_run[nt][i];
+          ml[(warp * R + n) * 2 + 1] = l;
+        }
+      }
+    const bool whole = ua == 0 && ub == nu;
+    const int slot = 2 * blockIdx.x + (first_part ? 0 : 1);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          merge[(warp * 8 + 2 * j + (q & 1)) * 132 + 16 * s + r + 8 * (q >> 1)] = o[s][nt][q];
+      __syncthreads();
+      // warp w: row w of this group of eight, four dims a lane
+      const int n = 8 * nt + warp, row = row0 + n;
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAttWarps; ++w) m = fmaxf(m, ml[(w * R + n) * 2]);
+      float l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kAttWarps; ++w) {
+        const float mw = ml[(w * R + n) * 2], f = mw == -INFINITY ? 0.f : ptx_exp2(mw - m);
+        const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + warp) * 132 + 4 * lane);
+        l = fmaf(f, ml[(w * R + n) * 2 + 1], l);
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
+      }
+      if (row < rows) {
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : a.v_scale / l;  // a NaN stays one
+          const int t = row / a.G, h = kvh * a.G + row - t * a.G;
+          *reinterpret_cast<uint2*>(a.o + b * a.ob + t * a.os + h * a.oh + 4 * lane) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (a.lse != nullptr && lane == 0)
+            a.lse[(static_cast<int64_t>(b) * a.Hkv * a.G + h) * a.Lq + t] =
+                l == 0.f ? -INFINITY : (m - kAttPShift + log2f(l)) * 0.69314718055994530942f;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * R + n) * 128 + 4 * lane) = acc;
+          if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + (static_cast<int64_t>(slot) * R + n) * 2) = make_float2(m, l);
+        }
+      }
+    }
+    first_part = false;
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
+// Joins the parts of split items: one CTA per (request, KV head, row tile)
+// and row; thread = dim.  The CTAs whose runs meet the item follow from the
+// same prefix sums; their parts are added in order.
+template <int NT>
+__global__ void __launch_bounds__(128) kv4_combine_kernel(const __grid_constant__ Kv4AttArgs a) {
+  constexpr int R = 8 * NT;
+  __shared__ int64_t sums[4];
+  extern __shared__ int32_t prefix[];
+  const int HT = a.Hkv * a.tiles;
+  const int item = blockIdx.x;  // b * HT + ht
+  const int b = item / HT, ht = item - b * HT, kvh = ht / a.tiles, tile = ht - kvh * a.tiles;
+  const int n = blockIdx.y, rows = a.G * a.Lq, row = tile * R + n;
+  // every block waits for the main kernel, so this grid never ends before it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row >= rows) return;
+  att_units(a, prefix, sums);
+  const int64_t total = static_cast<int64_t>(prefix[a.B]) * HT;
+  const int nu = prefix[b + 1] - prefix[b];
+  const int64_t u0 = static_cast<int64_t>(prefix[b]) * HT + static_cast<int64_t>(ht) * nu, u1 = u0 + nu;
+  // CTA c holds [total c / ctas, total (c + 1) / ctas): the one holding unit u is the last c with total c / ctas <= u
+  auto owner = [&](int64_t u) { return static_cast<int>(((u + 1) * a.ctas - 1) / total); };
+  const int c0 = owner(u0), c1 = owner(u1 - 1);
+  if (c0 == c1) return;  // whole in one CTA: written there
+  // the part is its CTA's first one unless the CTA's run began before the item
+  auto slot_of = [&](int c) { return 2 * c + (total * c / a.ctas < u0 ? 1 : 0); };
+  float m = -INFINITY;
+  for (int c = c0; c <= c1; ++c) {
+    if (total * c / a.ctas >= total * (c + 1) / a.ctas) continue;  // a CTA with no units
+    m = fmaxf(m, a.part_ml[(static_cast<int64_t>(slot_of(c)) * R + n) * 2]);
+  }
+  float l = 0.f, acc = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    if (total * c / a.ctas >= total * (c + 1) / a.ctas) continue;
+    const int64_t at = static_cast<int64_t>(slot_of(c)) * R + n;
+    const float2 x = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+    const float f = x.x == -INFINITY ? 0.f : ptx_exp2(x.x - m);
+    l = fmaf(f, x.y, l);
+    acc = fmaf(f, a.part_o[at * 128 + threadIdx.x], acc);
+  }
+  const int t = row / a.G, h = kvh * a.G + row - t * a.G;
+  a.o[b * a.ob + t * a.os + h * a.oh + threadIdx.x] = __float2bfloat16(l == 0.f ? 0.f : acc * (a.v_scale / l));
+  if (a.lse != nullptr && threadIdx.x == 0)
+    a.lse[(static_cast<int64_t>(b) * a.Hkv * a.G + h) * a.Lq + t] =
+        l == 0.f ? -INFINITY : (m - kAttPShift + log2f(l)) * 0.69314718055994530942f;
+}
+
+}  // namespace rbs

@@ -13,7 +13,10 @@
 
 #include "attention.cuh"
 #include "common.cuh"
+#include "kv4.cuh"
+#include "kv4_attend.cuh"
 #include "lists.cuh"
+#include "qknorm.cuh"
 #include "rope.cuh"
 #include "select.cuh"
 #include "stats.cuh"
@@ -101,6 +104,12 @@ rbs_status device_info(DeviceInfo** out) {
     for (auto kern : {topk_rows_kernel<2>, topk_rows_kernel<8>, topk_rows_kernel<32>, topk_rows_kernel<64>})
       e = e ? e : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(topk_smem_bytes(kTokMaxKV, kTokMaxKV / 32)));
+    e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     AttSmem<1>::bytes(kAttMaxBatch));
+    e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     AttSmem<2>::bytes(kAttMaxBatch));
+    e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     AttSmem<4>::bytes(kAttMaxBatch));
     e = e ? e : cudaFuncSetAttribute(block_beta_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RBS_MAX_KV_BLOCKS * 4);
     e = e ? e : cudaFuncSetAttribute(select_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RBS_MAX_KV_BLOCKS * 4);
     if (e != cudaSuccess) return fail(RBS_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -1072,6 +1081,308 @@ rbs_status rope_reencode(const rbs_bf16_tensor* x_in, rbs_bf16_tensor* x_out, co
   if (rope_style == 0) rope_reencode_kernel<0><<<grid, 256, 0, stream>>>(a);
   else rope_reencode_kernel<1><<<grid, 256, 0, stream>>>(a);
   return check_launch("rope_reencode_kernel");
+}
+
+// ---------------------------------------------------------------------------
+
+rbs_status rope_qk_norm(const rbs_bf16_tensor* q_in, rbs_bf16_tensor* q_out, const rbs_bf16_tensor* k_in,
+                        rbs_bf16_tensor* k_out, const void* q_weight, const void* k_weight, float eps,
+                        const int32_t* pos, int64_t pos_stride_b, float theta, int32_t rope_style,
+                        rbs_stream_t stream) {
+  rbs_status st;
+  if ((st = check_tensor(q_in, "q_in")) != RBS_OK) return st;
+  if ((st = check_tensor(q_out, "q_out")) != RBS_OK) return st;
+  if ((st = check_tensor(k_in, "k_in")) != RBS_OK) return st;
+  if ((st = check_tensor(k_out, "k_out")) != RBS_OK) return st;
+  RBS_REQUIRE(q_in->batch == q_out->batch && q_in->seqlen == q_out->seqlen && q_in->heads == q_out->heads,
+              RBS_ERR_INVALID_ARG, "q_out shape != q_in shape");
+  RBS_REQUIRE(k_in->batch == k_out->batch && k_in->seqlen == k_out->seqlen && k_in->heads == k_out->heads,
+              RBS_ERR_INVALID_ARG, "k_out shape != k_in shape");
+  RBS_REQUIRE(q_in->batch == k_in->batch && q_in->seqlen == k_in->seqlen, RBS_ERR_INVALID_ARG,
+              "queries and keys must be of the same tokens");
+  RBS_REQUIRE(pos != nullptr, RBS_ERR_INVALID_ARG, "null positions");
+  RBS_REQUIRE(pos_stride_b == 0 || pos_stride_b >= q_in->seqlen, RBS_ERR_INVALID_ARG,
+              "pos_stride_b must be 0 or at least the length");
+  RBS_REQUIRE(aligned16(q_weight) && aligned16(k_weight), RBS_ERR_INVALID_ARG, "weights not 16-byte aligned");
+  RBS_REQUIRE(eps >= 0.f && std::isfinite(eps), RBS_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  RBS_REQUIRE(theta > 0.f && std::isfinite(theta), RBS_ERR_INVALID_ARG, "theta must be positive and finite");
+  RBS_REQUIRE(rope_style == 0 || rope_style == 1, RBS_ERR_INVALID_ARG, "rope_style must be 0 or 1");
+  for (int x = 0; x < 2; ++x) {
+    const rbs_bf16_tensor *i = x ? k_in : q_in, *o = x ? k_out : q_out;
+    RBS_REQUIRE(i->data != o->data ||
+                    (i->stride_b == o->stride_b && i->stride_s == o->stride_s && i->stride_h == o->stride_h),
+                RBS_ERR_INVALID_ARG, "in-place rotation needs identical strides");
+  }
+  DeviceInfo* di;
+  if ((st = device_info(&di)) != RBS_OK) return st;
+  QkNormArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q_in->data);
+  a.k = static_cast<const __nv_bfloat16*>(k_in->data);
+  a.qo = static_cast<__nv_bfloat16*>(q_out->data);
+  a.ko = static_cast<__nv_bfloat16*>(k_out->data);
+  a.qb = q_in->stride_b; a.qs = q_in->stride_s; a.qh = q_in->stride_h;
+  a.kb = k_in->stride_b; a.ks = k_in->stride_s; a.kh = k_in->stride_h;
+  a.qob = q_out->stride_b; a.qos = q_out->stride_s; a.qoh = q_out->stride_h;
+  a.kob = k_out->stride_b; a.kos = k_out->stride_s; a.koh = k_out->stride_h;
+  a.wq = static_cast<const uint4*>(q_weight);
+  a.wk = static_cast<const uint4*>(k_weight);
+  a.pos = pos;
+  a.pos_b = pos_stride_b;
+  a.L = static_cast<int>(q_in->seqlen);
+  a.Hq = static_cast<int>(q_in->heads);
+  a.Hkv = static_cast<int>(k_in->heads);
+  a.per = kQkHeads;
+  a.nq = (a.Hq + a.per - 1) / a.per;
+  a.nk = (a.Hkv + a.per - 1) / a.per;
+  a.units = q_in->batch * q_in->seqlen * (a.nq + a.nk);
+  a.eps = eps;
+  // thread c's frequencies: pairs 8 c + i, or 4 c + i and 32 + 4 c + i
+  const double ln = std::log(static_cast<double>(theta)), inv_2pi = 0.15915494309189533577;
+  for (int i = 0; i < 8; ++i) {
+    const int first = rope_style == 0 ? 8 * i : 4 * i, then = rope_style == 0 || i < 4 ? i : 28 + i;
+    a.base[i] = std::exp(-2.0 * first / RBS_HEAD_DIM * ln) * inv_2pi;
+    a.step[i] = std::exp(-2.0 * then / RBS_HEAD_DIM * ln);
+  }
+  const int64_t grid = (a.units + kQkThreads / 8 - 1) / (kQkThreads / 8);
+  RBS_REQUIRE(grid < (1ll << 31), RBS_ERR_UNSUPPORTED, "too many head rows");
+  if (rope_style == 0) qk_norm_rope_kernel<0><<<static_cast<unsigned>(grid), kQkThreads, 0, stream>>>(a);
+  else qk_norm_rope_kernel<1><<<static_cast<unsigned>(grid), kQkThreads, 0, stream>>>(a);
+  return check_launch("qk_norm_rope_kernel");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// the 4-bit cache
+
+namespace {
+
+bool power_of_two(float x) {
+  int e;
+  return std::isfinite(x) && x >= 0x1p-64f && x <= 0x1p64f && std::frexp(x, &e) == 0.5f;
+}
+
+rbs_status check_page_size(int32_t page_size) {
+  RBS_REQUIRE(page_size >= kSubTokens && page_size <= RBS_KV4_MAX_PAGE && page_size % kSubTokens == 0, RBS_ERR_UNSUPPORTED,
+              "page_size must be a multiple of 16 between 16 and %d", RBS_KV4_MAX_PAGE);
+  return RBS_OK;
+}
+
+rbs_status check_cache(const rbs_kv4_cache* c) {
+  RBS_REQUIRE(c != nullptr && c->data != nullptr, RBS_ERR_INVALID_ARG, "cache: null");
+  RBS_REQUIRE(aligned16(c->data), RBS_ERR_INVALID_ARG, "cache: data not 16-byte aligned");
+  RBS_REQUIRE(c->num_pages > 0 && c->kv_heads > 0, RBS_ERR_INVALID_ARG, "cache: empty");
+  const rbs_status st = check_page_size(c->page_size);
+  if (st != RBS_OK) return st;
+  RBS_REQUIRE(c->num_pages <= ((1ll << 31) - 1) / c->page_size && c->kv_heads < (1 << 16), RBS_ERR_UNSUPPORTED,
+              "cache: more than 2^31 - 1 slots or 65535 heads");
+  RBS_REQUIRE(power_of_two(c->k_scale) && power_of_two(c->v_scale), RBS_ERR_INVALID_ARG,
+              "cache: k_scale and v_scale must be powers of two in [2^-64, 2^64]");
+  return RBS_OK;
+}
+
+rbs_status kv4_io(const rbs_kv4_cache* c, const rbs_bf16_tensor* K, const rbs_bf16_tensor* V, const int32_t* slots,
+                  Kv4IoArgs* a, unsigned* grid) {
+  rbs_status st;
+  if ((st = check_cache(c)) != RBS_OK) return st;
+  if ((st = check_tensor(K, "K")) != RBS_OK) return st;
+  if ((st = check_tensor(V, "V")) != RBS_OK) return st;
+  RBS_REQUIRE(K->batch == V->batch && K->seqlen == V->seqlen && K->heads == V->heads, RBS_ERR_INVALID_ARG,
+              "K/V shape mismatch");
+  RBS_REQUIRE(K->heads == c->kv_heads, RBS_ERR_INVALID_ARG, "K has %lld heads, the cache %d",
+              static_cast<long long>(K->heads), c->kv_heads);
+  RBS_REQUIRE(slots != nullptr, RBS_ERR_INVALID_ARG, "null slots");
+  a->data = static_cast<uint8_t*>(c->data);
+  a->num_slots = c->num_pages * c->page_size;
+  a->Hkv = c->kv_heads;
+  a->page = c->page_size;
+  a->slots = slots;
+  a->k = static_cast<__nv_bfloat16*>(K->data);
+  a->v = static_cast<__nv_bfloat16*>(V->data);
+  a->kb = K->stride_b; a->ks = K->stride_s; a->kh = K->stride_h;
+  a->vb = V->stride_b; a->vs = V->stride_s; a->vh = V->stride_h;
+  a->L = static_cast<int>(K->seqlen);
+  a->rows = K->batch * K->seqlen * K->heads;
+  a->kg = c->k_scale;
+  a->vg = c->v_scale;
+  a->kg_inv = 1.f / c->k_scale;
+  a->vg_inv = 1.f / c->v_scale;
+  const int64_t g = (a->rows + kIoThreads / 8 - 1) / (kIoThreads / 8);
+  RBS_REQUIRE(g < (1ll << 31), RBS_ERR_UNSUPPORTED, "too many head rows");
+  *grid = static_cast<unsigned>(g);
+  return RBS_OK;
+}
+
+// Query rows of one tile: the narrowest that holds a KV head's rows, at most
+// 32 (the outputs of 32 rows fill half of a thread's registers).
+int attend_tiles_n(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+int attend_ctas(const DeviceInfo* di, int nt) { return di->sms * (nt <= 2 ? 2 : 1); }
+constexpr int kAttMaxCtas = 2 * 160;  // workspace sizes need no device
+
+}  // namespace
+
+extern "C" {
+
+int64_t rbs_kv4_page_bytes(int32_t page_size) {
+  return check_page_size(page_size) == RBS_OK ? static_cast<int64_t>(page_size) / kSubTokens * kSubBytes : -1;
+}
+
+rbs_status kv4_extend(int32_t* block_table, int64_t table_stride, int32_t batch, int32_t max_pages,
+                      const int32_t* old_lens, const int32_t* new_lens, const int32_t* free_pages, int64_t num_free,
+                      const int32_t* free_head, int32_t page_size, int32_t max_new, int32_t* slots, int32_t* pos,
+                      int32_t* free_head_out, rbs_stream_t stream) {
+  RBS_REQUIRE(block_table != nullptr && old_lens != nullptr && new_lens != nullptr && free_pages != nullptr &&
+                  free_head != nullptr && slots != nullptr && pos != nullptr && free_head_out != nullptr,
+              RBS_ERR_INVALID_ARG, "null pointer");
+  RBS_REQUIRE(batch > 0 && max_pages > 0 && max_new > 0 && num_free > 0, RBS_ERR_INVALID_ARG, "empty shape");
+  RBS_REQUIRE(batch < (1 << 16) && num_free < (1ll << 31), RBS_ERR_UNSUPPORTED, "shape too large");
+  RBS_REQUIRE(table_stride >= max_pages, RBS_ERR_INVALID_ARG, "table_stride < max_pages");
+  rbs_status st = check_page_size(page_size);
+  if (st != RBS_OK) return st;
+  RBS_REQUIRE(static_cast<int64_t>(max_pages) * page_size < (1ll << 31), RBS_ERR_UNSUPPORTED,
+              "a request would pass 2^31 - 1 tokens");
+  RBS_REQUIRE(free_head != free_head_out, RBS_ERR_INVALID_ARG, "free_head_out may not be free_head");
+  DeviceInfo* di;
+  if ((st = device_info(&di)) != RBS_OK) return st;
+  ExtendArgs a;
+  a.table = block_table;
+  a.table_b = table_stride;
+  a.B = batch;
+  a.max_pages = max_pages;
+  a.page = page_size;
+  a.max_new = max_new;
+  a.old_lens = old_lens;
+  a.new_lens = new_lens;
+  a.free_pages = free_pages;
+  a.free_head = free_head;
+  a.num_free = num_free;
+  a.slots = slots;
+  a.pos = pos;
+  a.head_out = free_head_out;
+  // about two waves of CTAs: requests first, then slices of a request's slots
+  const int want = 2 * di->sms;
+  const int per_cta = std::min(kExtThreads, std::max(1, (batch + want - 1) / want));
+  const int gx = (batch + per_cta - 1) / per_cta;
+  const int gy = std::max(1, std::min({want / gx, (max_new + kExtThreads - 1) / kExtThreads, 65535}));
+  kv4_extend_kernel<<<dim3(gx, gy), kExtThreads, 0, stream>>>(a, per_cta);
+  return check_launch("kv4_extend_kernel");
+}
+
+rbs_status kv4_append(const rbs_kv4_cache* cache, const rbs_bf16_tensor* K, const rbs_bf16_tensor* V,
+                      const int32_t* slots, rbs_stream_t stream) {
+  Kv4IoArgs a;
+  unsigned grid;
+  DeviceInfo* di;
+  rbs_status st;
+  if ((st = kv4_io(cache, K, V, slots, &a, &grid)) != RBS_OK) return st;
+  if ((st = device_info(&di)) != RBS_OK) return st;
+  kv4_append_kernel<<<grid, kIoThreads, 0, stream>>>(a);
+  return check_launch("kv4_append_kernel");
+}
+
+rbs_status kv4_load(const rbs_kv4_cache* cache, const int32_t* slots, rbs_bf16_tensor* K, rbs_bf16_tensor* V,
+                    rbs_stream_t stream) {
+  Kv4IoArgs a;
+  unsigned grid;
+  DeviceInfo* di;
+  rbs_status st;
+  if ((st = kv4_io(cache, K, V, slots, &a, &grid)) != RBS_OK) return st;
+  if ((st = device_info(&di)) != RBS_OK) return st;
+  kv4_load_kernel<<<grid, kIoThreads, 0, stream>>>(a);
+  return check_launch("kv4_load_kernel");
+}
+
+size_t rbs_kv4_attend_workspace_bytes(int64_t seqlen_q, int64_t heads_q, int64_t kv_heads) {
+  if (seqlen_q <= 0 || heads_q <= 0 || kv_heads <= 0 || heads_q % kv_heads != 0) return 0;
+  const int nt = attend_tiles_n(heads_q / kv_heads * seqlen_q);
+  // two parts per CTA: 8 nt rows of 128 sums, then their (max, sum) pairs
+  return static_cast<size_t>(2) * kAttMaxCtas * 8 * nt * (RBS_HEAD_DIM + 2) * sizeof(float);
+}
+
+rbs_status kv4_attend(const rbs_bf16_tensor* Q, const rbs_kv4_cache* cache, const int32_t* block_table,
+                      int64_t table_stride, int32_t max_pages, const int32_t* lens, const int32_t* starts,
+                      int32_t window, int32_t sinks, float softmax_scale, void* workspace, size_t workspace_bytes,
+                      rbs_bf16_tensor* O, float* lse, rbs_stream_t stream) {
+  rbs_status st;
+  if ((st = check_tensor(Q, "Q")) != RBS_OK) return st;
+  if ((st = check_cache(cache)) != RBS_OK) return st;
+  if ((st = check_tensor(O, "O")) != RBS_OK) return st;
+  RBS_REQUIRE(O->batch == Q->batch && O->seqlen == Q->seqlen && O->heads == Q->heads, RBS_ERR_INVALID_ARG,
+              "O shape != Q shape");
+  RBS_REQUIRE(Q->heads % cache->kv_heads == 0, RBS_ERR_INVALID_ARG, "heads_q %% heads_kv != 0");
+  RBS_REQUIRE(block_table != nullptr && lens != nullptr, RBS_ERR_INVALID_ARG, "null block table or lengths");
+  RBS_REQUIRE(max_pages > 0 && table_stride >= max_pages, RBS_ERR_INVALID_ARG, "table_stride < max_pages or no pages");
+  RBS_REQUIRE(window >= 0 && sinks >= 0, RBS_ERR_INVALID_ARG, "window and sinks must be >= 0");
+  RBS_REQUIRE(std::isfinite(softmax_scale), RBS_ERR_INVALID_ARG, "softmax_scale must be finite");
+  RBS_REQUIRE(Q->batch <= kAttMaxBatch, RBS_ERR_UNSUPPORTED, "more than %d requests", kAttMaxBatch);
+  const int64_t G = Q->heads / cache->kv_heads, rows = G * Q->seqlen;
+  const int nt = attend_tiles_n(rows);
+  const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
+  RBS_REQUIRE(static_cast<int64_t>(max_pages) * cache->page_size < (1ll << 31) &&
+                  Q->batch * (static_cast<int64_t>(max_pages) * cache->page_size / (kAttWarps * kSubTokens) + 2) < (1ll << 31) &&
+                  Q->batch * cache->kv_heads * tiles < (1ll << 31),
+              RBS_ERR_UNSUPPORTED, "shape too large");
+  const size_t need = rbs_kv4_attend_workspace_bytes(Q->seqlen, Q->heads, cache->kv_heads);
+  RBS_REQUIRE(workspace != nullptr && aligned16(workspace), RBS_ERR_INVALID_ARG, "workspace null or not 16-byte aligned");
+  RBS_REQUIRE(workspace_bytes >= need, RBS_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  DeviceInfo* di;
+  if ((st = device_info(&di)) != RBS_OK) return st;
+  Kv4AttArgs a;
+  a.data = static_cast<const uint8_t*>(cache->data);
+  a.num_pages = cache->num_pages;
+  a.Hkv = cache->kv_heads;
+  a.G = static_cast<int>(G);
+  a.page = cache->page_size;
+  a.spp = cache->page_size / kSubTokens;
+  a.spp_magic = a.spp == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + a.spp - 1) / a.spp);
+  a.table = block_table;
+  a.table_b = table_stride;
+  a.max_pages = max_pages;
+  a.B = static_cast<int>(Q->batch);
+  a.Lq = static_cast<int>(Q->seqlen);
+  a.lens = lens;
+  a.starts = starts;
+  a.window = window;
+  a.sinks = sinks;
+  a.q = static_cast<const __nv_bfloat16*>(Q->data);
+  a.qb = Q->stride_b; a.qs = Q->stride_s; a.qh = Q->stride_h;
+  a.o = static_cast<__nv_bfloat16*>(O->data);
+  a.ob = O->stride_b; a.os = O->stride_s; a.oh = O->stride_h;
+  a.lse = lse;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(RBS_HEAD_DIM));
+  a.scale_log2 = scale * 1.4426950408889634f * cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.tiles = static_cast<int>(tiles);
+  a.ctas = std::min(attend_ctas(di, nt), kAttMaxCtas);
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + static_cast<int64_t>(2) * a.ctas * 8 * nt * RBS_HEAD_DIM;
+  const int64_t items = Q->batch * cache->kv_heads * tiles;
+  const int prefix_bytes = (a.B + 1) * 4;
+  // the combining kernel may start while the main one ends: it waits for it itself
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items), static_cast<unsigned>(8 * nt));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = prefix_bytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (nt == 1) {
+    kv4_attend_kernel<1><<<a.ctas, kAttThreads, AttSmem<1>::bytes(a.B), stream>>>(a);
+    e = cudaLaunchKernelEx(&cfg, kv4_combine_kernel<1>, a);
+  } else if (nt == 2) {
+    kv4_attend_kernel<2><<<a.ctas, kAttThreads, AttSmem<2>::bytes(a.B), stream>>>(a);
+    e = cudaLaunchKernelEx(&cfg, kv4_combine_kernel<2>, a);
+  } else {
+    kv4_attend_kernel<4><<<a.ctas, kAttThreads, AttSmem<4>::bytes(a.B), stream>>>(a);
+    e = cudaLaunchKernelEx(&cfg, kv4_combine_kernel<4>, a);
+  }
+  if ((st = check_launch("kv4_attend_kernel")) != RBS_OK) return st;
+  if (e != cudaSuccess) return fail(RBS_ERR_CUDA, "kv4_combine_kernel: %s", cudaGetErrorString(e));
+  return RBS_OK;
 }
 
 }  // extern "C"

@@ -76,10 +76,13 @@ typedef enum {
 } rbs_status;
 
 /* Device error word bits (rbs_get_device_error). */
-#define RBS_DEVERR_BLOCK_INDEX 0x1   /* a list entry outside [0, num_kv_blocks) */
+#define RBS_DEVERR_BLOCK_INDEX 0x1   /* a list entry outside [0, num_kv_blocks), or a page outside the cache */
 #define RBS_DEVERR_ROW_PTR 0x2       /* row_ptr not monotone or beyond capacity */
 #define RBS_DEVERR_TIMEOUT 0x4       /* a pipeline wait ran out of time */
 #define RBS_DEVERR_NONCAUSAL 0x8     /* a causal row lists a block after its diagonal */
+#define RBS_DEVERR_SLOT 0x10         /* a cache slot beyond the cache's pages */
+#define RBS_DEVERR_LENGTH 0x20       /* a request length that is negative, shrinks or passes its block table */
+#define RBS_DEVERR_PAGES 0x40        /* the list of free pages ran out */
 
 typedef struct {
   void* data; /* device pointer to the element at [0, 0, 0, 0] */
@@ -380,6 +383,115 @@ RBS_API rbs_status bsa_prefill_segments(const rbs_bf16_tensor* Q, const rbs_bf16
  * Re-encoding from old_pos = 0 is plain RoPE encoding. */
 RBS_API rbs_status rope_reencode(const rbs_bf16_tensor* x_in, rbs_bf16_tensor* x_out, const int32_t* old_pos,
                          const int32_t* new_pos, float theta, int32_t rope_style, rbs_stream_t stream);
+
+/* ---- norm of queries and keys with the position rotation, one pass
+ * No counterpart in the papers: what a model with per-head norms does to a
+ * projection's queries and keys before any call of this library, the encoding
+ * that rope_reencode moves later.  For every head row x of the token at
+ * position p:
+ *   y = rot_p(w * x / sqrt(mean(x^2) + eps))
+ * with w the queries' or the keys' 128 norm weights and rot_p the rotation of
+ * rope_reencode from position 0 to p (same theta, same rope_style).  fp32
+ * throughout, the angle formed and reduced in fp64, rounded to bf16 once.
+ *   q_in, q_out  [B, L, Hq, 128] bf16, k_in, k_out [B, L, Hkv, 128] bf16 (views of one packed
+ *                projection will do); an output may be its input (same strides)
+ *   q_weight, k_weight  [128] bf16, 16-byte aligned, or NULL for all ones
+ *   eps          finite, >= 0
+ *   pos          int32 positions, token l of batch entry b at pos[b * pos_stride_b + l]; pos_stride_b 0
+ *                shares [L] between the entries (any sign: the rotation is by p as given) */
+RBS_API rbs_status rope_qk_norm(const rbs_bf16_tensor* q_in, rbs_bf16_tensor* q_out, const rbs_bf16_tensor* k_in,
+                                rbs_bf16_tensor* k_out, const void* q_weight, const void* k_weight, float eps,
+                                const int32_t* pos, int64_t pos_stride_b, float theta, int32_t rope_style,
+                                rbs_stream_t stream);
+
+/* ---- a paged key/value cache held in 4 bits
+ * No counterpart in the papers: where the keys and values of the prefill (or
+ * of retrieved passages, [BA] 2.5 Inference) stay for the tokens that follow.
+ * A key or value of one token and KV head is 8 groups of 16 dims; a group
+ * holds e2m1 codes q (0, .5, 1, 1.5, 2, 3, 4, 6, with sign) and one e4m3 scale
+ * s, and stands for q * s * g with g = k_scale or v_scale:
+ *   s = e4m3(amax / (6 g)), to nearest even, 448 at most
+ *   q = e2m1(x / (s g)), to nearest even, 6 at most in size; 0 when s is 0
+ * g is a power of two (1 suits values around 1: groups with amax between
+ * 0.1 g and 2688 g keep the full precision of s).  A group that holds a NaN
+ * or an infinity reads back as NaN.  What a group stands for is exact in bf16
+ * (within bf16's range).
+ * The cache is a caller-owned buffer [num_pages, kv_heads, page bytes], page
+ * bytes = rbs_kv4_page_bytes(page_size) = page_size / 16 * 2304, 16-byte
+ * aligned; no byte is shared by two tokens.  page_size is a multiple of 16, at
+ * most RBS_KV4_MAX_PAGE.  A slot is page * page_size + offset; num_pages *
+ * page_size stays below 2^31.  A sub-block of 16 tokens of a (page, head):
+ *   [0, 1024)     key codes, token 8h + r: byte 512 h + 64 r + 16 j + 2 s + e holds
+ *                 dims 16s + 8e + 2j (low half) and the next (high half)
+ *   [1024, 2048)  value codes, token 8h + 2j + i: byte 512 h + 64 r + 16 j + 8 i + s holds
+ *                 dims 16s + r (low half) and 16s + 8 + r (high half)
+ *   [2048, 2176)  key scales, token t, group s: byte 8 t + s
+ *   [2176, 2304)  value scales, token 2a + i, group s: byte 16 a + 2 s + i */
+#define RBS_KV4_MAX_PAGE 256
+typedef struct {
+  void* data;
+  int64_t num_pages;
+  int32_t kv_heads, page_size;
+  float k_scale, v_scale; /* powers of two in [2^-64, 2^64] */
+} rbs_kv4_cache;
+/* Bytes of one page of one KV head; -1 for a page size that is not allowed. */
+RBS_API int64_t rbs_kv4_page_bytes(int32_t page_size);
+
+/* Pages and slots for requests that grow from old_lens to new_lens tokens (old 0: a new request).  Request b's
+ * entries ceil(old / page_size) .. ceil(new / page_size) - 1 of the block table get the next pages of the free
+ * list, requests in order, from free_pages[*free_head] on; then
+ *   slots[b, i], pos[b, i] = slot and position of token old + i   (i < new - old)
+ *                            -1, -1                                (other i < max_new).
+ *   block_table  [batch, max_pages] int32, rows table_stride apart, entries of tokens held valid; updated in place
+ *   old_lens, new_lens  [batch] int32
+ *   free_pages   [num_free] int32; free_head [1] int32, pages of the list taken so far; free_head_out [1] the same
+ *                after the call (another buffer than free_head)
+ *   slots, pos   out [batch, max_new] int32, contiguous
+ * A list that runs out gives entries and slots of -1 and RBS_DEVERR_PAGES; a length that is negative, below the
+ * old one, beyond max_pages * page_size or more than max_new above the old one is brought into range (tokens past
+ * max_new get pages and no slots) with RBS_DEVERR_LENGTH.  One launch, no scratch; the same call may be repeated. */
+RBS_API rbs_status kv4_extend(int32_t* block_table, int64_t table_stride, int32_t batch, int32_t max_pages,
+                              const int32_t* old_lens, const int32_t* new_lens, const int32_t* free_pages,
+                              int64_t num_free, const int32_t* free_head, int32_t page_size, int32_t max_new,
+                              int32_t* slots, int32_t* pos, int32_t* free_head_out, rbs_stream_t stream);
+
+/* Write tokens to the cache, and read tokens back from it.
+ *   K, V   [B, L, kv_heads, 128] bf16; the inputs of kv4_append, the outputs of kv4_load
+ *   slots  [B, L] int32, contiguous.  A negative slot is padding: kv4_append skips the token, kv4_load returns
+ *          zeros.  A slot beyond the cache raises RBS_DEVERR_SLOT and is treated as padding.
+ * The slots of one kv4_append must be distinct (two tokens with one slot leave it holding parts of both);
+ * kv4_load takes any. */
+RBS_API rbs_status kv4_append(const rbs_kv4_cache* cache, const rbs_bf16_tensor* K, const rbs_bf16_tensor* V,
+                              const int32_t* slots, rbs_stream_t stream);
+RBS_API rbs_status kv4_load(const rbs_kv4_cache* cache, const int32_t* slots, rbs_bf16_tensor* K, rbs_bf16_tensor* V,
+                            rbs_stream_t stream);
+
+/* Attention of new tokens over the cache.  Query t of request b is the token at position p = starts[b] + t
+ * (lens[b] - Lq + t without starts) and sees the cached keys s with
+ *   s <= p                        window == 0
+ *   s <= p and (s > p - window or s < sinks)   window > 0.
+ *   O[b, t, h] = sum_s softmax_s(scale * q . k_s) v_s,   KV head = h / (Hq / Hkv).
+ * A query with p < 0 or p >= lens[b] sees nothing: O is 0 and lse -inf (padded rows of a batch, requests of
+ * length 0).  Bytes of keys that no query sees do not matter.
+ *   Q            [B, Lq, Hq, 128] bf16, B <= 4096.  Meant for one to a few tokens per request: rows of
+ *                (token, q head of the group) share one pass over the cache in tiles of 32.
+ *   block_table  [B, max_pages] int32, rows table_stride apart: pages of tokens page_size i ..; entries past a
+ *                request's length are not read.  A page outside the cache raises RBS_DEVERR_BLOCK_INDEX and its
+ *                keys are left out.
+ *   lens         [B] int32, tokens held including the new ones; out of [0, max_pages * page_size] is brought into
+ *                range with RBS_DEVERR_LENGTH
+ *   starts       [B] int32 or NULL
+ *   softmax_scale  <= 0 selects 1/sqrt(128)
+ *   workspace    rbs_kv4_attend_workspace_bytes(...) bytes, 16-byte aligned, needs no initialisation; calls that
+ *                may overlap on the GPU need one each
+ *   O            out [B, Lq, Hq, 128] bf16 (may not alias Q)
+ *   lse          optional out [B, Hq, Lq] fp32 = ln sum_s exp(scale q . k_s)
+ * Results do not depend on what else the GPU runs: parts are joined in a fixed order. */
+RBS_API size_t rbs_kv4_attend_workspace_bytes(int64_t seqlen_q, int64_t heads_q, int64_t kv_heads);
+RBS_API rbs_status kv4_attend(const rbs_bf16_tensor* Q, const rbs_kv4_cache* cache, const int32_t* block_table,
+                              int64_t table_stride, int32_t max_pages, const int32_t* lens, const int32_t* starts,
+                              int32_t window, int32_t sinks, float softmax_scale, void* workspace,
+                              size_t workspace_bytes, rbs_bf16_tensor* O, float* lse, rbs_stream_t stream);
 
 /* ---- testing hooks (no counterpart in the papers; used by the library's
  * own tests to reach code paths that correct inputs never reach)

@@ -1,0 +1,365 @@
+"""GPU parity of the 4-bit cache with the fp64 oracle: pages and slots,
+writing and reading tokens (to the byte), and attention over it."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_long_rbs_b200 as rbs
+from helpers import host_bits
+from oracle import serving_oracle as S
+from serving_helpers import FP16, check_attention, f64, ints, randn
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- writing and reading tokens
+
+
+def _special(rng, B, L, H):
+    """Values of every size: unequal channels, zero groups, borders of the codes, sizes at and past the scales' ends."""
+    x = rng.standard_normal((B, L, H, 128)) * np.exp(rng.standard_normal(128))
+    x[0, 0, 0, :16] = 0
+    x[0, 0, 0, 16:32] = [6, -6, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, -.25, -.75, -1.25, -1.75, -2.5, -3.5, -5]
+    x[0, 0, 0, 32:48] = 1e4
+    x[0, 0, 0, 48:64] = rng.standard_normal(16) * 1e-3
+    x[0, 0, 0, 64:80] = rng.standard_normal(16) * 1e-6
+    x[0, 0, 0, 80:96] = -0.0
+    # scales on the border between two e4m3 values: amax = 6 * (s + half a step)
+    for i in range(16):
+        x[-1, -1, -1, 8 * i:8 * i + 8] = 6 * (1 + (2 * i + 1) / 16) * 2.0 ** (i - 8)
+    return torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("B,L,H,page,gk,gv", [(1, 1, 1, 16, 1.0, 1.0), (2, 37, 3, 48, 0.25, 4.0),
+                                              (5, 9, 4, 256, 2.0 ** -20, 2.0 ** 20), (1, 130, 2, 64, 1.0, 2.0)])
+def test_append_writes_the_documented_bytes_and_load_reads_them(cuda_ok, B, L, H, page, gk, gv):
+    rng = np.random.default_rng(L + page)
+    K, V = _special(rng, B, L, H), _special(rng, B, L, H)
+    pages = -(-B * L // page) + 2
+    slots = rng.permutation(pages * page)[:B * L].reshape(B, L)
+    if L > 8:
+        slots[-1, -3:-1] = [-1, -77]  # padding
+    cache = rbs.KV4Cache.empty(pages, page, H, k_scale=gk, v_scale=gv)
+    cache.data.fill_(0xA5)
+    rbs.kv4_append(cache, K, V, ints(slots))
+    (kc, ks), (vc, vs) = S.quantise(f64(K), gk), S.quantise(f64(V), gv)
+    want = np.full(tuple(cache.data.shape), 0xA5, dtype=np.uint8)
+    for b in range(B):
+        for t in range(L):
+            for h in range(H):
+                if slots[b, t] >= 0:
+                    S.write_token(want, slots[b, t], page, h, kc[b, t, h], ks[b, t, h], vc[b, t, h], vs[b, t, h])
+    assert np.array_equal(cache.data.cpu().numpy(), want)
+    k, v = rbs.kv4_load(cache, ints(slots))
+    there = (slots >= 0)[:, :, None, None]
+    assert np.array_equal(f64(k), np.where(there, S.values(kc, ks, gk), 0))
+    assert np.array_equal(f64(v), np.where(there, S.values(vc, vs, gv), 0))
+    assert rbs.rbs_get_device_error() == 0
+
+
+def test_nan_and_infinity_take_their_group(cuda_ok):
+    rng = np.random.default_rng(3)
+    K, V = randn(rng, 1, 4, 1, 128), randn(rng, 1, 4, 1, 128)
+    K[0, 1, 0, 20], V[0, 2, 0, 127] = float("inf"), float("nan")
+    cache = rbs.KV4Cache.empty(1, 16, 1)
+    slots = ints([[3, 2, 9, 8]])
+    rbs.kv4_append(cache, K, V, slots)
+    for x, y in zip((K, V), rbs.kv4_load(cache, slots)):
+        assert np.array_equal(f64(y), S.round_trip(f64(x)), equal_nan=True)
+
+
+def test_views_and_strides(cuda_ok):
+    """Keys and values as views of a packed projection; outputs in another head order."""
+    rng = np.random.default_rng(4)
+    qkv = randn(rng, 2, 21, 10, 128)
+    K, V = qkv[:, :, 6:8], qkv[:, :, 8:]
+    cache = rbs.KV4Cache.empty(4, 16, 2)
+    slots = ints(rng.permutation(64)[:42].reshape(2, 21))
+    rbs.kv4_append(cache, K, V, slots)
+    hold = torch.full((2, 2, 30, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    k, v = rbs.kv4_load(cache, slots, k_out=hold.transpose(1, 2)[:, 3:24])
+    assert np.array_equal(f64(k), S.round_trip(f64(K))) and np.array_equal(f64(v), S.round_trip(f64(V)))
+    assert (hold[:, :, :3] == 7).all() and (hold[:, :, 24:] == 7).all()
+
+
+def test_slots_past_the_cache_are_reported_and_skipped(cuda_ok):
+    rng = np.random.default_rng(5)
+    K = randn(rng, 1, 3, 2, 128)
+    cache = rbs.KV4Cache.empty(2, 16, 2)
+    cache.data.zero_()
+    rbs.rbs_get_device_error()
+    bad = ints([[32, 5, (1 << 31) - 1]])
+    rbs.kv4_append(cache, K, K, bad)
+    assert rbs.rbs_get_device_error() == rbs.DEVERR_SLOT
+    k, _ = rbs.kv4_load(cache, bad)
+    assert rbs.rbs_get_device_error() == rbs.DEVERR_SLOT
+    assert not f64(k)[0, [0, 2]].any() and np.array_equal(f64(k)[0, 1], S.round_trip(f64(K)[0, 1]))
+
+
+# ---- pages and slots
+
+
+def _extend_case(rng, B, page, width, max_new):
+    old = rng.integers(0, width * page - max_new + 1, B) * (rng.random(B) > 0.3)
+    new = old + rng.integers(0, max_new + 1, B)
+    need = -(-new // page) - -(-old // page)
+    had = -(-old // page)
+    pages = rng.permutation(int(had.sum() + need.sum()) + 3)
+    table = np.full((B, width), -1)
+    at = 0
+    for b in range(B):
+        table[b, :had[b]] = pages[at:at + had[b]]
+        at += had[b]
+    free = np.concatenate([rng.permutation(7) + 10000, pages[at:]])  # seven pages of the list are taken
+    return table, old, new, free, 7
+
+
+@pytest.mark.parametrize("B,page,width,max_new", [(1, 16, 1, 1), (1, 64, 700, 40000), (64, 64, 20, 1), (300, 16, 9, 33),
+                                                  (1000, 48, 5, 100), (3, 256, 10, 513), (2049, 16, 3, 2)])
+def test_extend(cuda_ok, B, page, width, max_new):
+    rng = np.random.default_rng(B + max_new)
+    table, old, new, free, head = _extend_case(rng, B, page, width, max_new)
+    t = ints(table)
+    args = (ints(old), ints(new), ints(free), ints([head]), max_new, page)
+    want = S.extend(table, old, new, free, head, max_new, page)
+    rbs.rbs_get_device_error()
+    for _ in range(2):  # the same call again changes nothing
+        slots, pos, out = rbs.kv4_extend(t, *args)
+        for got, w in zip((t, slots, pos), want):
+            assert np.array_equal(got.cpu().numpy(), w)
+        assert out.item() == want[3]
+    assert rbs.rbs_get_device_error() == 0
+
+
+def test_extend_row_views(cuda_ok):
+    rng = np.random.default_rng(1)
+    table, old, new, free, head = _extend_case(rng, 5, 16, 6, 20)
+    hold = torch.full((5, 11), -9, dtype=torch.int32, device="cuda")
+    hold[:, :6] = ints(table)
+    rbs.kv4_extend(hold[:, :6], ints(old), ints(new), ints(free), ints([head]), 20, 16)
+    want = S.extend(table, old, new, free, head, 20, 16)
+    assert np.array_equal(hold[:, :6].cpu().numpy(), want[0]) and (hold[:, 6:] == -9).all()
+
+
+def test_extend_errors(cuda_ok):
+    """A list that runs out, and lengths out of range: reported, and nothing beyond the buffers is touched."""
+    rbs.rbs_get_device_error()
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    i0 = ints([0, 0, 0])
+    slots, pos, head = rbs.kv4_extend(table, i0, ints([16, 40, 17]), ints([5, 6, 7]), ints([0]), 40, 16)
+    assert rbs.rbs_get_device_error() == rbs.DEVERR_PAGES
+    assert table.cpu().tolist() == [[5, -1, -1, -1], [6, 7, -1, -1], [-1, -1, -1, -1]] and head.item() == 3
+    s = slots.cpu().numpy()
+    assert (s[0, :16] == 80 + np.arange(16)).all() and (s[1, :32] >= 0).all() and (s[1, 32:] == -1).all()
+    assert (s[2] == -1).all() and pos.cpu().numpy()[2, :17].tolist() == list(range(17))
+    rbs.kv4_extend(table, i0, i0, ints([5]), ints([2]), 1, 16)
+    assert rbs.rbs_get_device_error() == rbs.DEVERR_PAGES  # the count itself is past the list
+    for old, new, want in (([-3, 0, 0], [1, 0, 0], [1, 0, 0]), ([9, 0, 0], [4, 0, 0], [0, 0, 0]),
+                           ([0, 0, 0], [0, 0, 9], [0, 0, 8]), ([62, 0, 0], [70, 1, 0], [2, 1, 0])):
+        slots, _, _ = rbs.kv4_extend(table.zero_(), ints(old), ints(new), ints(np.arange(9)), ints([0]), 8, 16)
+        assert rbs.rbs_get_device_error() == rbs.DEVERR_LENGTH
+        assert (slots >= 0).sum(1).tolist() == want
+
+
+# ---- attention
+
+
+class Held:
+    """Requests of the given lengths in a cache whose other bytes are 0xff (NaN scales), and what it holds in fp64."""
+
+    def __init__(self, rng, lens, H, page, width=None, gk=1.0, gv=1.0, k_scale=1.0):
+        self.lens, B = np.asarray(lens), len(lens)
+        need = -(-self.lens // page)
+        self.width = max(1, int(need.max())) if width is None else width
+        total = int(need.sum())
+        order = rng.permutation(total + 2)
+        self.table = np.full((B, self.width), 1 << 30)
+        at = 0
+        for b in range(B):
+            self.table[b, :need[b]] = order[at:at + need[b]]
+            at += need[b]
+        self.cache = rbs.KV4Cache.empty(total + 2, page, H, k_scale=gk, v_scale=gv)
+        self.cache.data.fill_(0xFF)
+        n = max(1, int(self.lens.max()))
+        K, V = randn(rng, B, n, H, 128, scale=k_scale), randn(rng, B, n, H, 128)
+        t = np.arange(n)
+        slots = np.where(t < self.lens[:, None],
+                         self.table[np.arange(B)[:, None], np.minimum(t // page, self.width - 1)] * page + t % page, -1)
+        self.slots = slots
+        rbs.kv4_append(self.cache, K, V, ints(slots))
+        self.k, self.v = S.round_trip(f64(K), gk), S.round_trip(f64(V), gv)
+
+    def expect(self, Q, starts=None, window=0, sinks=0, scale=None):
+        Q = f64(Q)
+        B, Lq, Hq, D = Q.shape
+        G = Hq // self.k.shape[2]
+        scale = D ** -0.5 if scale is None else scale
+        out, a = np.zeros_like(Q), np.zeros_like(Q)
+        lse, z = np.zeros((B, Hq, Lq)), np.zeros((B, Hq, Lq))
+        for b in range(B):
+            n = int(self.lens[b])
+            qp = (n - Lq if starts is None else starts[b]) + np.arange(Lq)
+            see = S.visible(qp, np.arange(n), window, sinks) & ((qp >= 0) & (qp < n))[:, None]
+            for h in range(Hq):
+                o, e, aa, zz = S.attend(Q[b, :, h], self.k[b, :n, h // G], self.v[b, :n, h // G], see, scale)
+                out[b, :, h], lse[b, h], a[b, :, h], z[b, h] = o, e, aa, zz
+        return out, lse, a, z
+
+
+def _check(o, lse, held, Q, what="", **kw):
+    """A weight p (relative to the running maximum; the row sum is at least 1) is held as fp16 of 2^6 p: below fp16's
+    normal range it is off by up to half of 2^-24 instead of p * 2^-11, so by 2^-31 of the largest weight for each key."""
+    floor = 2.0 ** -31 * np.abs(held.v[np.isfinite(held.v)]).max(initial=0) * held.lens.max()
+    check_attention(o, lse, held.expect(Q, **kw), FP16, what, floor)
+
+
+def _attend(held, Q, starts=None, **kw):
+    o, lse = rbs.kv4_attend(Q, held.cache, ints(held.table), ints(held.lens),
+                            starts=None if starts is None else ints(starts), return_lse=True, **kw)
+    return o, lse
+
+
+@pytest.mark.parametrize("G", [1, 2, 5, 8, 16, 40])
+@pytest.mark.parametrize("Lq", [1, 3])
+def test_attend_heads_and_tokens(cuda_ok, G, Lq):
+    rng = np.random.default_rng(G * 10 + Lq)
+    held = Held(rng, [1, 15, 16, 17, 0, 128, 129, 500, 2], 2, 16)
+    Q = randn(rng, 9, Lq, 2 * G, 128)
+    o, lse = _attend(held, Q)
+    _check(o, lse, held, Q)
+    assert not f64(o)[4].any() and rbs.rbs_get_device_error() == 0
+
+
+@pytest.mark.parametrize("page", [16, 32, 48, 64, 112, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 1), (16, 4), (100, 0), (100, 40), (333, 1000), (5000, 4)])
+def test_attend_windows_and_pages(cuda_ok, page, window, sinks):
+    rng = np.random.default_rng(page + window + sinks)
+    held = Held(rng, [700, 1, 333, 64, 350], 1, page)
+    Q = randn(rng, 5, 2, 4, 128)
+    o, lse = _attend(held, Q, window=window, sinks=sinks)
+    _check(o, lse, held, Q, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("lens,H,G,Lq", [([20000], 1, 8, 1), ([9001, 3], 2, 4, 2), ([5000] * 3, 4, 1, 1),
+                                         ([30, 4000, 700, 1, 0, 2500], 8, 2, 1), ([6000, 100], 1, 8, 9),
+                                         ([2000], 1, 3, 50)])
+def test_attend_split_over_many_blocks(cuda_ok, lens, H, G, Lq):
+    rng = np.random.default_rng(len(lens) + G + Lq)
+    held = Held(rng, lens, H, 64)
+    Q = randn(rng, len(lens), Lq, H * G, 128)
+    o, lse = _attend(held, Q)
+    _check(o, lse, held, Q)
+    again, lse2 = _attend(held, Q)
+    assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
+def test_attend_starts_and_padded_rows(cuda_ok):
+    """Queries left-aligned in a padded batch: rows past a request's length and before its first token are empty."""
+    rng = np.random.default_rng(20)
+    held = Held(rng, [40, 7, 0, 300], 2, 32)
+    Q = randn(rng, 4, 5, 4, 128)
+    for starts in ([35, 5, 0, 100], [-2, 0, 3, 298], [40, 50, -9, (1 << 31) - 1], [-(1 << 31), 6, 0, 299]):
+        for kw in ({}, dict(window=3, sinks=2)):
+            o, lse = _attend(held, Q, starts=starts, **kw)
+            _check(o, lse, held, Q, str(starts), starts=starts, **kw)
+
+
+@pytest.mark.parametrize("qs,ks", [(30.0, 1.0), (1e-20, 1.0), (1e20, 1e-3), (1.0, 100.0)])
+def test_attend_score_sizes(cuda_ok, qs, ks):
+    """Peaked and flat rows, and queries far outside fp16's range."""
+    rng = np.random.default_rng(21)
+    held = Held(rng, [777, 50], 1, 48, k_scale=ks)
+    Q = randn(rng, 2, 1, 8, 128, scale=qs)
+    scale = 1e-18 if qs > 1e10 else 0.3
+    o, lse = _attend(held, Q, softmax_scale=scale)
+    _check(o, lse, held, Q, scale=scale)
+
+
+def test_attend_rising_scores_and_scales(cuda_ok):
+    """Keys whose scores rise along the cache (every block moves the maximum); k_scale, v_scale other than 1."""
+    rng = np.random.default_rng(22)
+    held = Held(rng, [900], 1, 64, gk=0.125, gv=8.0)
+    q = f64(randn(rng, 1, 1, 1, 128))[0, 0, 0]
+    K = np.linspace(-3, 3, 900)[None, :, None, None] * q + 0.1 * rng.standard_normal((1, 900, 1, 128))
+    K, V = (torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda() for x in (K, rng.standard_normal((1, 900, 1, 128))))
+    rbs.kv4_append(held.cache, K, V, ints(held.slots))
+    held.k, held.v = S.round_trip(f64(K), 0.125), S.round_trip(f64(V), 8.0)
+    Q = torch.from_numpy(np.stack([q, -q, 0 * q]).astype(np.float32)).to(torch.bfloat16).cuda().view(1, 1, 3, 128)
+    o, lse = _attend(held, Q)
+    _check(o, lse, held, Q)
+
+
+def test_nan_in_masked_places_stays_there(cuda_ok):
+    """NaN keys and values reach the queries that see them and no others: not earlier drafted tokens, not rows whose
+    window has passed them."""
+    rng = np.random.default_rng(23)
+    held = Held(rng, [60, 60], 1, 16)
+    K, V = randn(rng, 2, 60, 1, 128), randn(rng, 2, 60, 1, 128)
+    K[0, 58, 0, 3] = float("nan")
+    V[1, 57, 0, 30] = float("nan")
+    V[1, 20, 0, 90] = float("inf")
+    rbs.kv4_append(held.cache, K, V, ints(held.slots))
+    held.k, held.v = S.round_trip(f64(K)), S.round_trip(f64(V))
+    Q = randn(rng, 2, 8, 2, 128)
+    for kw in ({}, dict(window=36), dict(window=36, sinks=21)):
+        o, _ = _attend(held, Q, **kw)
+        for b in range(2):
+            for t in range(8):
+                p = 52 + t
+                see = S.visible([p], np.arange(60), kw.get("window", 0), kw.get("sinks", 0))[0]
+                hit = np.isnan(held.v[b, see, 0]).any(0) | np.isnan(held.k[b, see, 0]).any()
+                assert np.array_equal(np.isnan(f64(o)[b, t]), np.broadcast_to(hit, (2, 128))), (b, t, kw)
+
+
+def test_bad_pages_and_lengths(cuda_ok):
+    rng = np.random.default_rng(24)
+    held = Held(rng, [200, 90], 2, 32)
+    Q = randn(rng, 2, 1, 4, 128)
+    want = held.expect(Q)
+    rbs.rbs_get_device_error()
+    held.table[0, 2] = held.cache.data.shape[0]  # tokens 64 .. 95 of request 0 are nowhere
+    o, lse = _attend(held, Q)
+    assert rbs.rbs_get_device_error() == rbs.DEVERR_BLOCK_INDEX
+    keep = np.r_[0:64, 96:200]
+    short = Held.__new__(Held)
+    short.lens, short.k, short.v = np.array([168]), held.k[:1, keep], held.v[:1, keep]
+    r = short.expect(Q[:1])
+    check_attention(o[:1], lse[:1], r, FP16)
+    check_attention(o[1:], lse[1:], tuple(x[1:] for x in want), FP16)
+    held.table[0, 2] = -5
+    _attend(held, Q)
+    assert rbs.rbs_get_device_error() == rbs.DEVERR_BLOCK_INDEX
+    held.table[0, 2] = 0
+    for n in (-1, 7 * 32 + 1):
+        held.lens[1] = n
+        _attend(held, Q)
+        assert rbs.rbs_get_device_error() & rbs.DEVERR_LENGTH
+
+
+def test_attend_layouts_streams_graph(cuda_ok):
+    """Queries as a view of a packed projection, outputs in another order, a given workspace, another stream, and a
+    graph replayed on changed lengths."""
+    rng = np.random.default_rng(25)
+    held = Held(rng, [300, 45], 2, 16, width=40)
+    qkv = randn(rng, 2, 1, 20, 128)
+    Q = qkv[:, :, 2:18]
+    want, lse = _attend(held, Q)
+    _check(want, lse, held, Q)
+    hold = torch.zeros(2, 16, 3, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((rbs.rbs_kv4_attend_workspace_bytes(1, 16, 2),), 255, dtype=torch.uint8, device="cuda")
+    table, lens = ints(held.table), ints(held.lens)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        rbs.kv4_attend(Q, held.cache, table, lens, out=hold.transpose(1, 2)[:, 1:2], workspace=ws)
+    s.synchronize()
+    assert torch.equal(hold.transpose(1, 2)[:, 1:2], want) and not hold[:, :, [0, 2]].any()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, z = rbs.kv4_attend(Q, held.cache, table, lens, return_lse=True)
+    for n in ([300, 45], [17, 0], [299, 32]):
+        lens.copy_(ints(n))
+        g.replay()
+        a, b = rbs.kv4_attend(Q, held.cache, table, lens, return_lse=True)
+        assert torch.equal(o, a) and torch.equal(z, b)
