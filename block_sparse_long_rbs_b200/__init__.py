@@ -37,7 +37,7 @@ __all__ = [
     "SelectParams", "BlockLists", "rbs_block_stats", "rbs_block_beta", "rbs_pool_queries", "rbs_select",
     "rbs_select_capacity", "rbs_select_workspace_bytes", "rbs_lists_causal_full", "rbs_lists_block_attention",
     "bsa_prefill", "bsa_prefill_rescue_weighted", "bsa_prefill_segments", "rope_reencode", "rbs_get_device_error",
-    "rope_qk_norm", "KV4Cache", "rbs_kv4_page_bytes", "kv4_extend", "kv4_append", "kv4_load", "kv4_attend",
+    "rope_qk_norm", "swa_prefill", "KV4Cache", "rbs_kv4_page_bytes", "kv4_extend", "kv4_append", "kv4_load", "kv4_attend",
     "rbs_kv4_attend_workspace_bytes", "RbsError",
 ]
 
@@ -421,6 +421,24 @@ def rope_qk_norm(Q: torch.Tensor, K: torch.Tensor, q_weight: torch.Tensor | None
     _call(dev, lib().rope_qk_norm, "rope_qk_norm", tq, to, tk, tp, w[0], w[1], eps, p_ptr, 0 if shared else L, theta,
           rope_style)
     return q_out, k_out
+
+
+def swa_prefill(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, window: int, sinks: int = 0, q_offset: int = 0,
+                softmax_scale: float | None = None, out: torch.Tensor | None = None, return_lse: bool = False):
+    """Causal attention of Q [B, Lq, Hq, 128] over K, V [B, Lk, Hkv, 128] where the query at position p = t + q_offset
+    sees the last `window` keys up to its own and the first `sinks` (window 0: every key up to its own)."""
+    tq, tk, tv = _t(Q, "Q"), _t(K, "K"), _t(V, "V")
+    dev = Q.device
+    if out is None:
+        out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+    B, Lq, Hq, D = Q.shape
+    lse = torch.empty(B, Hq, Lq, dtype=torch.float32, device=dev) if return_lse else None
+    to = _t(out, "out")
+    if K.device != dev or V.device != dev or out.device != dev:
+        _one_device("Q", Q, K=K, V=V, out=out)
+    _call(dev, lib().swa_prefill, "swa_prefill", tq, tk, tv, window, sinks, q_offset,
+          1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale, to, None if lse is None else lse.data_ptr())
+    return (out, lse) if return_lse else out
 
 
 def rbs_kv4_page_bytes(page_size: int) -> int:

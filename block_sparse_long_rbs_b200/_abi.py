@@ -78,6 +78,8 @@ SIGNATURES = {
     "rope_reencode": (ctypes.c_int, [P(Bf16Tensor), P(Bf16Tensor), vp, vp, f32, i32, vp]),
     "rope_qk_norm": (ctypes.c_int, [P(Bf16Tensor), P(Bf16Tensor), P(Bf16Tensor), P(Bf16Tensor), vp, vp, f32, vp, i64,
                                     f32, i32, vp]),
+    "swa_prefill": (ctypes.c_int, [P(Bf16Tensor), P(Bf16Tensor), P(Bf16Tensor), i32, i32, i64, f32, P(Bf16Tensor), vp,
+                                   vp]),
     "rbs_kv4_page_bytes": (i64, [i32]),
     "kv4_extend": (ctypes.c_int, [vp, i64, i32, i32, vp, vp, vp, i64, vp, i32, i32, vp, vp, vp, vp]),
     "kv4_append": (ctypes.c_int, [P(KV4CacheC), P(Bf16Tensor), P(Bf16Tensor), vp, vp]),

@@ -22,6 +22,7 @@
 #include "stats.cuh"
 #include "select_mma.cuh"
 #include "tokmax.cuh"
+#include "window.cuh"
 
 using namespace rbs;
 
@@ -104,6 +105,7 @@ rbs_status device_info(DeviceInfo** out) {
     for (auto kern : {topk_rows_kernel<2>, topk_rows_kernel<8>, topk_rows_kernel<32>, topk_rows_kernel<64>})
       e = e ? e : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(topk_smem_bytes(kTokMaxKV, kTokMaxKV / 32)));
+    e = e ? e : cudaFuncSetAttribute(swa_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WinSmem::kAlloc);
     e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      AttSmem<1>::bytes(kAttMaxBatch));
     e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1148,6 +1150,99 @@ rbs_status rope_qk_norm(const rbs_bf16_tensor* q_in, rbs_bf16_tensor* q_out, con
   if (rope_style == 0) qk_norm_rope_kernel<0><<<static_cast<unsigned>(grid), kQkThreads, 0, stream>>>(a);
   else qk_norm_rope_kernel<1><<<static_cast<unsigned>(grid), kQkThreads, 0, stream>>>(a);
   return check_launch("qk_norm_rope_kernel");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// sliding window
+
+namespace {
+
+// 4-D map over [B, L, H, 128] bf16 with a box of 64 dims x `heads` heads x
+// `rows` tokens, 128-byte swizzle: rows ordered (token, head).
+rbs_status make_group_map(const rbs_bf16_tensor* t, int heads, int rows, CUtensorMap* map) {
+  PFN_encodeTiled enc = encode_fn();
+  if (enc == nullptr) return fail(RBS_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[4] = {RBS_HEAD_DIM, static_cast<cuuint64_t>(t->heads), static_cast<cuuint64_t>(t->seqlen),
+                              static_cast<cuuint64_t>(t->batch)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(t->stride_h) * 2, static_cast<cuuint64_t>(t->stride_s) * 2,
+                                 static_cast<cuuint64_t>(t->stride_b) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(RBS_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return RBS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rbs_status swa_prefill(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const rbs_bf16_tensor* V, int32_t window,
+                       int32_t sinks, int64_t q_offset, float softmax_scale, rbs_bf16_tensor* O, float* lse,
+                       rbs_stream_t stream) {
+  rbs_status st;
+  if ((st = check_tensor(Q, "Q")) != RBS_OK) return st;
+  if ((st = check_tensor(K, "K")) != RBS_OK) return st;
+  if ((st = check_tensor(V, "V")) != RBS_OK) return st;
+  if ((st = check_tensor(O, "O")) != RBS_OK) return st;
+  RBS_REQUIRE(K->batch == Q->batch && V->batch == Q->batch && O->batch == Q->batch, RBS_ERR_INVALID_ARG, "batch mismatch");
+  RBS_REQUIRE(K->seqlen == V->seqlen && K->heads == V->heads, RBS_ERR_INVALID_ARG, "K/V shape mismatch");
+  RBS_REQUIRE(O->seqlen == Q->seqlen && O->heads == Q->heads, RBS_ERR_INVALID_ARG, "O shape != Q shape");
+  RBS_REQUIRE(Q->heads % K->heads == 0, RBS_ERR_INVALID_ARG, "heads_q %% heads_kv != 0");
+  RBS_REQUIRE(window >= 0 && sinks >= 0, RBS_ERR_INVALID_ARG, "window and sinks must be >= 0");
+  RBS_REQUIRE(q_offset >= 0, RBS_ERR_INVALID_ARG, "q_offset must be >= 0");
+  RBS_REQUIRE(std::isfinite(softmax_scale), RBS_ERR_INVALID_ARG, "softmax_scale must be finite");
+  const int64_t G = Q->heads / K->heads;
+  RBS_REQUIRE(G <= 128, RBS_ERR_UNSUPPORTED, "more than 128 q heads share a KV head");
+  // positions, and a tile past either end, fit 32 bits
+  RBS_REQUIRE(q_offset + Q->seqlen + 512 < (1ll << 31) && K->seqlen + 512 < (1ll << 31), RBS_ERR_UNSUPPORTED,
+              "positions beyond 2^31");
+  RBS_REQUIRE(Q->stride_h <= Q->stride_s && K->stride_h <= K->stride_s && V->stride_h <= V->stride_s,
+              RBS_ERR_UNSUPPORTED, "Q/K/V must have the head stride no larger than the token stride ([B, L, H, 128] order)");
+  WinArgs a;
+  a.T = static_cast<int>(128 / G);
+  a.nt = static_cast<int>((Q->seqlen + a.T - 1) / a.T);
+  const int64_t items = Q->batch * K->heads * a.nt;
+  RBS_REQUIRE(items < (1ll << 30), RBS_ERR_UNSUPPORTED, "shape too large");
+  DeviceInfo* di;
+  if ((st = device_info(&di)) != RBS_OK) return st;
+  int si;
+  if ((st = make_group_map(Q, static_cast<int>(G), a.T, &a.tmQ)) != RBS_OK) return st;
+  for (int x = 0; x < 2; ++x) {
+    const rbs_bf16_tensor* t = x == 0 ? K : V;
+    if ((st = make_tensor_map(t, kWinKeys, x == 0 ? &a.tmK : &a.tmV, &si)) != RBS_OK) return st;
+    if ((st = make_tensor_map(t, kWinSinkRows, x == 0 ? &a.tmKs : &a.tmVs, &si)) != RBS_OK) return st;
+    if ((st = make_tensor_map(t, kWinKeys - kWinSinkRows, x == 0 ? &a.tmKw : &a.tmVw, &si)) != RBS_OK) return st;
+  }
+  a.Q = static_cast<const __nv_bfloat16*>(Q->data);
+  a.K = static_cast<const __nv_bfloat16*>(K->data);
+  a.V = static_cast<const __nv_bfloat16*>(V->data);
+  a.O = static_cast<__nv_bfloat16*>(O->data);
+  a.qb = Q->stride_b; a.qs = Q->stride_s; a.qh = Q->stride_h;
+  a.kb = K->stride_b; a.ks = K->stride_s; a.kh = K->stride_h;
+  a.vb = V->stride_b; a.vs = V->stride_s; a.vh = V->stride_h;
+  a.ob = O->stride_b; a.os = O->stride_s; a.oh = O->stride_h;
+  a.lse = lse;
+  a.B = static_cast<int>(Q->batch);
+  a.G = static_cast<int>(G);
+  a.Hkv = static_cast<int>(K->heads);
+  a.Lq = static_cast<int>(Q->seqlen);
+  a.Lk = static_cast<int>(K->seqlen);
+  a.q_off = q_offset;
+  const int64_t end = q_offset + Q->seqlen;  // no window is wider than the positions it reaches
+  a.W = static_cast<int>(window == 0 ? end : std::min<int64_t>(window, end));
+  a.S = static_cast<int>(std::min<int64_t>(sinks, end));
+  a.items = static_cast<int>(items);
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(RBS_HEAD_DIM));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_ns = kWaitLimitNs;
+  const int grid = static_cast<int>(std::min<int64_t>(items, 2 * di->sms));
+  swa_prefill_kernel<<<grid, kWinThreads, WinSmem::kAlloc, stream>>>(a);
+  return check_launch("swa_prefill_kernel");
 }
 
 }  // extern "C"

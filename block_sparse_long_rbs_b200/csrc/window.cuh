@@ -1,0 +1,454 @@
+// Sliding-window attention with sinks on the 5th-generation tensor core:
+// query p sees the keys s <= p with p - W < s, and the first S keys.
+//
+// A work item is T = 128 / G tokens of one (batch, KV head): the 128 rows of
+// the tile are the (token, q head) pairs of the G q heads that share the KV
+// head.  The keys an item needs span T + W - 1 positions, so a narrow window
+// wastes little of a tile (128 tokens of one head would span 127 + W), and a
+// key tile is read once for all G heads.  Key tiles of 64 start at the item's
+// own first visible key (TMA rows may start anywhere).  Up to 16 sinks share a
+// tile with the window's first 48 keys; more sinks get tiles of their own.
+//
+// Two CTAs per SM, each a whole pipeline on half of the SM's tensor and shared
+// memory: while one CTA's softmax waits for its products or its epilogue
+// stores, the other one has the tensor core and the issue slots.  Within a
+// CTA two S buffers let S_{g+1} run under the softmax of tile g.
+// Roles (256 threads):
+//   warps 0-3  softmax: a thread owns one row (its TMEM lane).  It reads the 64
+//              scores, masks them in tiles that some row sees only in part,
+//              takes the maximum (the running maximum moves, and O is rescaled,
+//              only when it grows by more than 2^8), writes
+//              P = exp2(S c - m) as bf16 pairs over the scores, and at the end
+//              writes O / l and the LSE.
+//   warp 4     Q and K producer, warp 5 V producer (TMA, one lane)
+//   warp 6     TMEM allocator, issuer of S = Q K^T (both operands in shared memory)
+//   warp 7     issuer of O += P V (P in TMEM, V MN-major in shared memory)
+// TMEM columns: S buffers [0, 64) and [64, 128), O [128, 256).
+//
+// Masked scores are replaced before the softmax, so NaN keys stay out; a NaN or
+// infinite value in a masked place still meets a zero weight in the product.
+// Such a row comes out non-finite and is computed again by its warp from the
+// visible keys alone (window_exact_row), as is a row that is non-finite by right.
+// Every mbarrier wait is bounded, as in attention.cuh.
+#pragma once
+
+#include "common.cuh"
+
+namespace rbs {
+
+struct WinArgs {
+  // Q boxes of T tokens x G heads, K / V boxes of 64, 16 and 48 keys
+  CUtensorMap tmQ, tmK, tmV, tmKs, tmVs, tmKw, tmVw;
+  const __nv_bfloat16 *Q, *K, *V;
+  __nv_bfloat16* O;
+  int64_t qb, qs, qh, kb, ks, kh, vb, vs, vh, ob, os, oh;
+  float* lse;  // [B, Hq, Lq] or null
+  int B, G, Hkv, Lq, Lk, T, nt;  // T tokens per item, nt items per (batch, KV head)
+  int64_t q_off;
+  int W, S;
+  int items;
+  float scale_log2;
+  uint64_t wait_ns;
+};
+
+constexpr int kWinThreads = 256;
+constexpr int kWinKeys = 64;    // keys of a tile
+constexpr int kWinSinkRows = 16;  // rows that sinks take in a shared first tile
+constexpr int kWinNS = 2;       // K and V ring depth
+
+struct WinSmem {
+  static constexpr int kQBytes = 128 * 256;
+  static constexpr int kKVBytes = kWinKeys * 256;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kQBytes;
+  static constexpr int kV = kK + kWinNS * kKVBytes;
+  static constexpr int kBar = kV + kWinNS * kKVBytes;
+  static constexpr int kTotal = kBar + 256;
+  static constexpr int kAlloc = kTotal + 1024;
+  static constexpr uint32_t kTmemCols = 256;
+  __host__ __device__ static constexpr uint32_t col_s(int buf) { return buf * kWinKeys; }
+  static constexpr uint32_t kColO = 128;
+};
+static_assert(2 * (WinSmem::kAlloc + 1024) <= 228 * 1024, "two CTAs per SM");
+
+enum : int {
+  kWbQFull = 0,
+  kWbQEmpty = 1,
+  kWbKFull = 2,                // + stage
+  kWbVFull = kWbKFull + kWinNS,
+  kWbSFull = kWbVFull + kWinNS,  // + S buffer
+  kWbPFull = kWbSFull + 2,       // + S buffer
+  kWbPVDone = kWbPFull + 2,      // + tile mod 4
+  kWbOFull = kWbPVDone + 4,
+  kWbOEmpty = kWbOFull + 1,
+  kWbDrain = kWbOEmpty + 1,      // + issuer
+  kWbNum = kWbDrain + 2
+};
+static_assert(kWbNum * 8 + 16 <= 256, "barrier area");
+
+// One item's key tiles.  Positions fit 32 bits (q_off + Lq < 2^31, checked by
+// the host).
+struct WinItem {
+  int b, kvh, t0;      // batch, KV head, first token
+  int p0, p1;          // positions of the first and last token
+  int lo;              // first key of the window part
+  int sinks;           // sinks before the window part
+  int n_sink;          // tiles of sinks alone
+  bool merged;         // the first tile holds the sinks and 48 window keys
+  int n;               // tiles
+};
+
+__device__ __forceinline__ WinItem win_item(const WinArgs& a, int w) {
+  WinItem x;
+  const int per_b = a.Hkv * a.nt;
+  x.b = w / per_b;
+  const int rem = w - x.b * per_b;
+  x.kvh = rem / a.nt;
+  x.t0 = (a.nt - 1 - (rem - x.kvh * a.nt)) * a.T;  // the last tokens, with the most keys, first
+  x.p0 = static_cast<int>(a.q_off) + x.t0;
+  x.p1 = min(x.p0 + a.T, static_cast<int>(a.q_off) + a.Lq) - 1;
+  const int hi = min(x.p1, a.Lk - 1);
+  x.lo = max(0, x.p0 - a.W + 1);
+  if (x.lo < a.S) x.lo = 0;  // the sinks are, or adjoin, the window's first keys
+  x.sinks = min(min(a.S, x.lo), a.Lk);
+  const int len = max(0, hi - x.lo + 1);
+  x.merged = x.sinks > 0 && x.sinks <= kWinSinkRows && len > 0;
+  x.n_sink = x.merged ? 0 : (x.sinks + kWinKeys - 1) / kWinKeys;
+  x.n = x.n_sink + ((x.merged ? kWinSinkRows : 0) + len + kWinKeys - 1) / kWinKeys;
+  return x;
+}
+
+// Key of tile t's column 0 (of a merged first tile: what column 16 would give, minus 16).
+__device__ __forceinline__ int win_key0(const WinItem& x, int t) {
+  if (t < x.n_sink) return t * kWinKeys;
+  return x.lo - (x.merged ? kWinSinkRows : 0) + (t - x.n_sink) * kWinKeys;
+}
+
+// One row from the visible keys alone, by a whole warp: lane l holds dims
+// 4l .. 4l + 3.  Only rows whose fast result is not finite come here.
+__device__ __noinline__ void window_exact_row(const WinArgs& a, int b, int kvh, int h, int t) {
+  const int lane = threadIdx.x & 31;
+  const int p = static_cast<int>(a.q_off) + t, w0 = max(0, p - a.W + 1), hi = min(p, a.Lk - 1);
+  const uint2 qx = *reinterpret_cast<const uint2*>(a.Q + b * a.qb + t * a.qs + h * a.qh + 4 * lane);
+  const float q[4] = {bf16lo(qx.x), bf16hi(qx.x), bf16lo(qx.y), bf16hi(qx.y)};
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  auto take = [&](int s) {
+    const uint2 kx = *reinterpret_cast<const uint2*>(a.K + b * a.kb + s * a.ks + kvh * a.kh + 4 * lane);
+    float d = q[0] * bf16lo(kx.x) + q[1] * bf16hi(kx.x) + q[2] * bf16lo(kx.y) + q[3] * bf16hi(kx.y);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) d += __shfl_xor_sync(0xffffffffu, d, i);
+    d *= a.scale_log2;
+    const float mn = fmaxf(m, d), f = m == -INFINITY ? 0.f : ptx_exp2(m - mn), e = mn == -INFINITY ? (d == -INFINITY ? 0.f : d) : ptx_exp2(d - mn);
+    const uint2 vx = *reinterpret_cast<const uint2*>(a.V + b * a.vb + s * a.vs + kvh * a.vh + 4 * lane);
+    const float v[4] = {bf16lo(vx.x), bf16hi(vx.x), bf16lo(vx.y), bf16hi(vx.y)};
+    m = mn;
+    l = l * f + e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = o[i] * f + e * v[i];
+  };
+  for (int s = 0; s < min(min(a.S, w0), a.Lk); ++s) take(s);
+  for (int s = w0; s <= hi; ++s) take(s);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2*>(a.O + b * a.ob + t * a.os + h * a.oh + 4 * lane) =
+      make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+}
+
+__global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __grid_constant__ WinArgs a) {
+  using L = WinSmem;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase + L::kQ, sK = sbase + L::kK, sV = sbase + L::kV, bars = sbase + L::kBar;
+  auto bar = [&](int k) -> uint32_t { return bars + 8u * k; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBar + kWbNum * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kBar + kWbNum * 8 + 4);
+  const uint64_t limit = a.wait_ns;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    mbar_init(bar(kWbQFull), 1);
+    mbar_init(bar(kWbQEmpty), 1);
+    for (int s = 0; s < kWinNS; ++s) {
+      mbar_init(bar(kWbKFull + s), 1);
+      mbar_init(bar(kWbVFull + s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kWbSFull + s), 1);
+      mbar_init(bar(kWbPFull + s), 4);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(bar(kWbPVDone + s), 1);
+    mbar_init(bar(kWbOFull), 1);
+    mbar_init(bar(kWbOEmpty), 4);
+    mbar_init(bar(kWbDrain), 1);
+    mbar_init(bar(kWbDrain + 1), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  {
+    // Q rows past T G and V rows that no copy has filled yet would otherwise
+    // hold whatever ran here before: finite zeros once
+    uint4* z = reinterpret_cast<uint4*>(smem + L::kQ);
+    for (int k = tid; k < L::kBar / 16; k += kWinThreads) z[k] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  if (warp == 6) {
+    tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4 || warp == 5) {
+    // ------------------------------------------------------------ Q + K / V producers
+    if (lane == 0) {
+      const bool isK = warp == 4;
+      const CUtensorMap *map = isK ? &a.tmK : &a.tmV, *map_s = isK ? &a.tmKs : &a.tmVs, *map_w = isK ? &a.tmKw : &a.tmVw;
+      const uint32_t ring = isK ? sK : sV;
+      const int full0 = isK ? kWbKFull : kWbVFull;
+      tma_prefetch_desc(map);
+      if (isK) tma_prefetch_desc(&a.tmQ);
+      const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
+      uint32_t nf = 0, nq = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; w < a.items && ok; w += gridDim.x) {
+        const WinItem x = win_item(a, w);
+        if (x.n == 0) continue;
+        if (isK) {
+          if (nq >= 1 && !mbar_wait(bar(kWbQEmpty), (nq - 1) & 1, abort_flag, limit)) break;
+          mbar_arrive_expect_tx(bar(kWbQFull), a.T * a.G * 256);
+          tma_load_4d_hint(sQ, &a.tmQ, bar(kWbQFull), 0, x.kvh * a.G, x.t0, x.b, pol_q);
+          tma_load_4d_hint(sQ + 128 * 128, &a.tmQ, bar(kWbQFull), 64, x.kvh * a.G, x.t0, x.b, pol_q);
+          ++nq;
+        }
+        for (int t = 0; t < x.n; ++t) {
+          const int s = nf % kWinNS;
+          // the stage's previous tile is consumed: its S (for K) or PV (for V)
+          // is complete.  Neither barrier can move past that phase before this
+          // load lands, so the parity is unambiguous.
+          if (nf >= kWinNS) {
+            const uint32_t prev = nf - kWinNS;
+            const bool done = isK ? mbar_wait(bar(kWbSFull + (prev & 1)), (prev >> 1) & 1, abort_flag, limit)
+                                  : mbar_wait(bar(kWbPVDone + (prev & 3)), (prev >> 2) & 1, abort_flag, limit);
+            if (!done) { ok = false; break; }
+          }
+          mbar_arrive_expect_tx(bar(full0 + s), L::kKVBytes);
+          const uint32_t dst = ring + s * L::kKVBytes;
+          const int k0 = win_key0(x, t);
+          if (t == 0 && x.merged) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t d = dst + hf * kWinKeys * 128;
+              tma_load_4d_hint(d, map_s, bar(full0 + s), 64 * hf, x.kvh, 0, x.b, pol_kv);
+              tma_load_4d_hint(d + kWinSinkRows * 128, map_w, bar(full0 + s), 64 * hf, x.kvh, x.lo, x.b, pol_kv);
+            }
+          } else {
+            tma_load_4d_hint(dst, map, bar(full0 + s), 0, x.kvh, k0, x.b, pol_kv);
+            tma_load_4d_hint(dst + kWinKeys * 128, map, bar(full0 + s), 64, x.kvh, k0, x.b, pol_kv);
+          }
+          ++nf;
+        }
+      }
+      // every load issued must land before the CTA exits
+      for (uint32_t s = 0; s < kWinNS; ++s)
+        if (s < nf) mbar_drain(bar(full0 + s), ((nf - s + kWinNS - 1) / kWinNS - 1) & 1, limit);
+      if (isK && nq > 0) mbar_drain(bar(kWbQFull), (nq - 1) & 1, limit);
+    }
+  } else if (warp == 6 || warp == 7) {
+    // ------------------------------------------------------------ S issuer / PV issuer
+    const bool isS = warp == 6;
+    constexpr uint32_t idS = idesc_bf16_f32(128, kWinKeys, 0, 0);
+    constexpr uint32_t idPV = idesc_bf16_f32(128, 128, 0, 1);
+    const uint64_t qdesc = smem_desc(sQ, 16, 1024, kLayoutSW128);
+    const uint64_t kdesc0 = smem_desc(sK, 16, 1024, kLayoutSW128);
+    const uint64_t vdesc0 = smem_desc(sV, kWinKeys * 128, 1024, kLayoutSW128);
+    constexpr uint32_t kStageUnits = L::kKVBytes >> 4, kQHalf = (128 * 128) >> 4, kKHalf = (kWinKeys * 128) >> 4;
+    auto wait = [&](int k, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(k), parity, abort_flag, limit)); };
+    uint32_t g = 0, it = 0;  // tiles and items so far
+    bool ok = true;
+    for (int w = blockIdx.x; w < a.items && ok; w += gridDim.x) {
+      const WinItem x = win_item(a, w);
+      if (x.n == 0) continue;
+      for (int t = 0; t < x.n; ++t, ++g) {
+        const int b = g & 1, s = g % kWinNS;
+        if (isS) {
+          if (t == 0 && !wait(kWbQFull, it & 1)) { ok = false; break; }
+          if (!wait(kWbKFull + s, (g / kWinNS) & 1)) { ok = false; break; }
+          // S_g overwrites P_{g-2}: PV_{g-2} must be complete
+          if (g >= 2 && !wait(kWbPVDone + ((g - 2) & 3), ((g - 2) >> 2) & 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t kd = kdesc0 + s * kStageUnits;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ss_warp(tmem + L::col_s(b), qdesc + (kk >> 2) * kQHalf + (kk & 3) * 2, kd + (kk >> 2) * kKHalf + (kk & 3) * 2,
+                         idS, kk > 0 ? 1u : 0u);
+          umma_commit_warp(bar(kWbSFull + b));
+          if (t == x.n - 1) umma_commit_warp(bar(kWbQEmpty));
+        } else {
+          if (!wait(kWbPFull + b, (g >> 1) & 1)) { ok = false; break; }
+          if (!wait(kWbVFull + s, (g / kWinNS) & 1)) { ok = false; break; }
+          if (t == 0 && it > 0 && !wait(kWbOEmpty, (it - 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t vd = vdesc0 + s * kStageUnits;
+#pragma unroll
+          for (int kk = 0; kk < kWinKeys / 16; ++kk)
+            umma_ts_warp(tmem + L::kColO, tmem + L::col_s(b) + kk * 8, vd + kk * (2048 >> 4), idPV, (t == 0 && kk == 0) ? 0u : 1u);
+          umma_commit_warp(bar(kWbPVDone + (g & 3)));
+          if (t == x.n - 1) umma_commit_warp(bar(kWbOFull));
+        }
+      }
+      ++it;
+    }
+    // drain this issuer's tensor-core work before TMEM is freed
+    umma_commit_warp(bar(kWbDrain + (isS ? 0 : 1)));
+    mbar_drain(bar(kWbDrain + (isS ? 0 : 1)), 0, limit);
+  } else {
+    // ------------------------------------------------------------ softmax (warps 0-3)
+    const int r = tid;  // row of the tile == TMEM lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const float c = a.scale_log2;
+    const int tl = r / a.G, gh = r - tl * a.G;  // token and q head of this row
+    auto warp_arrive = [&](int k) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(k));
+    };
+    uint32_t g = 0, it = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; w < a.items && ok; w += gridDim.x) {
+      const WinItem x = win_item(a, w);
+      const int t_row = x.t0 + tl, h = x.kvh * a.G + gh;
+      const bool live = tl < a.T && t_row < a.Lq;
+      const int64_t lse_at = (static_cast<int64_t>(x.b) * a.G * a.Hkv + h) * a.Lq + t_row;
+      uint4* dst = reinterpret_cast<uint4*>(a.O + x.b * a.ob + t_row * a.os + h * a.oh);
+      if (x.n == 0) {
+        if (live) {
+          for (int k = 0; k < 16; ++k) dst[k] = make_uint4(0, 0, 0, 0);
+          if (a.lse != nullptr) a.lse[lse_at] = -INFINITY;
+        }
+        continue;
+      }
+      const int p = x.p0 + tl, hi = min(p, a.Lk - 1), w_lo = p - a.W + 1;
+      float m_used = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int t = 0; t < x.n; ++t, ++g) {
+        const int b = g & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kWbSFull + b), (g >> 1) & 1, abort_flag, limit))) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t scol = lane_base + L::col_s(b);
+        uint32_t v[2][32];
+        tmem_ld32(scol, v[0]);
+        tmem_ld32(scol + 32, v[1]);
+        tmem_wait_ld();
+        const int k0 = win_key0(x, t);
+        const bool sink_tile = t < x.n_sink, shared = t == 0 && x.merged;
+        if (sink_tile || shared || k0 + kWinKeys - 1 > min(x.p0, a.Lk - 1) || k0 <= x.p1 - a.W) {
+          // column e is hidden above hi_c, and below lo_c unless it is a sink
+          const int hi_c = hi - k0, lo_c = sink_tile ? kWinKeys : w_lo - k0;
+          const int sk_c = sink_tile ? x.sinks - k0 : shared ? x.sinks : a.S - k0;
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e > hi_c || (e < lo_c && e >= sk_c)) v[e >> 5][e & 31] = __float_as_uint(-INFINITY);
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
+        const float m_new = fmaxf(m_used, mx * c);
+        float factor = 1.f;
+        bool rescale = false;
+        if (t == 0) {
+          m_used = m_new;
+        } else if (m_new - m_used > 8.f) {
+          // a row that has seen no key yet has nothing to scale
+          rescale = m_used != -INFINITY;
+          factor = ptx_exp2(m_used - m_new);
+          m_used = m_new;
+        }
+        const float m_exp = m_used == -INFINITY ? 0.f : m_used;
+        l2.x *= factor;
+        l2.y *= factor;
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(-m_exp, -m_exp);
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pw[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const float2 arg = ffma2(make_float2(__uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1])), c2, nm2);
+          const float2 pv = make_float2(ptx_exp2(arg.x), ptx_exp2(arg.y));
+          acc[(e >> 1) & 1] = fadd2(acc[(e >> 1) & 1], pv);
+          pw[e >> 1] = pack_bf16x2(pv.x, pv.y);
+        }
+        tmem_st32(scol, pw);
+        l2 = fadd2(l2, fadd2(acc[0], acc[1]));
+        if (__any_sync(0xffffffffu, rescale)) {
+          // O must hold every earlier tile's product first.  The next phase of
+          // PV_{g-1}'s barrier is PV_{g+3}, which needs this tile's P.
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(kWbPVDone + ((g - 1) & 3)), ((g - 1) >> 2) & 1, abort_flag, limit))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + L::kColO + 32 * q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+            tmem_st32(lane_base + L::kColO + 32 * q, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(kWbPFull + b);
+      }
+      if (!ok) break;
+
+      // ---- epilogue: O / l -> bf16, LSE
+      const float l = l2.x + l2.y;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(kWbOFull), it & 1, abort_flag, limit))) { ok = false; break; }
+      tc_fence_after();
+      float odd = 0.f;  // stays 0 while every output is finite
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[32];
+        tmem_ld32(lane_base + L::kColO + 32 * q, o);
+        tmem_wait_ld();
+        if (q == 3) {
+          tc_fence_before();
+          warp_arrive(kWbOEmpty);
+        }
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          f[e] = __uint_as_float(o[e]) * inv;
+          odd = fmaf(f[e], 0.f, odd);
+        }
+        if (live) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            __stcs(dst + 4 * q + k, make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
+                                               pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7])));
+        }
+      }
+      if (live && a.lse != nullptr) a.lse[lse_at] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f;
+      for (uint32_t bad = __ballot_sync(0xffffffffu, live && odd != 0.f); bad != 0; bad &= bad - 1) {
+        const int src = __ffs(bad) - 1;
+        __syncwarp();
+        window_exact_row(a, x.b, x.kvh, __shfl_sync(0xffffffffu, h, src), __shfl_sync(0xffffffffu, t_row, src));
+      }
+      ++it;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 6) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+}  // namespace rbs

@@ -404,6 +404,24 @@ RBS_API rbs_status rope_qk_norm(const rbs_bf16_tensor* q_in, rbs_bf16_tensor* q_
                                 const int32_t* pos, int64_t pos_stride_b, float theta, int32_t rope_style,
                                 rbs_stream_t stream);
 
+/* ---- sliding-window attention with sinks
+ * No counterpart in the papers: the layers of a model whose queries see a
+ * window need no selection.  Query token t at position p = t + q_offset sees
+ * the keys s with
+ *   s <= p                                     window == 0
+ *   s <= p and (s > p - window or s < sinks)   window > 0
+ *   O[b, t, h] = sum_s softmax_s(scale * q_t . k_s) v_s,   KV head = h / (Hq / Hkv)
+ * in bf16 tensor-core products with fp32 accumulation and softmax.
+ *   Q         [B, Lq, Hq, 128] bf16; K, V [B, Lk, Hkv, 128] bf16; each with stride_h <= stride_s; Hq / Hkv <= 128;
+ *             any lengths and q_offset >= 0 (keys past Lk do not exist)
+ *   softmax_scale  <= 0 selects 1/sqrt(128)
+ *   O         out [B, Lq, Hq, 128] bf16 (may not alias Q, K or V)
+ *   lse       optional out [B, Hq, Lq] fp32 = ln sum_s exp(scale q_t.k_s) (-inf where no key is seen, O = 0)
+ * Keys and values that a query does not see do not reach it, NaN and infinities included.  Uses no workspace. */
+RBS_API rbs_status swa_prefill(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const rbs_bf16_tensor* V,
+                               int32_t window, int32_t sinks, int64_t q_offset, float softmax_scale,
+                               rbs_bf16_tensor* O, float* lse, rbs_stream_t stream);
+
 /* ---- a paged key/value cache held in 4 bits
  * No counterpart in the papers: where the keys and values of the prefill (or
  * of retrieved passages, [BA] 2.5 Inference) stay for the tokens that follow.

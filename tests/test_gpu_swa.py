@@ -1,0 +1,136 @@
+"""GPU parity of swa_prefill with the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_long_rbs_b200 as rbs
+from oracle import serving_oracle as S
+from serving_helpers import BF16, check_attention, f64, randn
+
+pytestmark = pytest.mark.gpu
+
+
+def _check(Q, K, V, window, sinks, off=0, scale=None, rows=None, **kw):
+    o, lse = rbs.swa_prefill(Q, K, V, window, sinks, q_offset=off, softmax_scale=scale, return_lse=True, **kw)
+    W = window if window else off + Q.shape[1]
+    ref = S.window_attention(f64(Q), f64(K), f64(V), W, sinks, off, scale, rows)
+    got = (o, lse) if rows is None else (o[:, rows], lse[:, :, rows])
+    check_attention(*got, ref, BF16)
+    assert rbs.rbs_get_device_error() == 0
+    return o, lse
+
+
+def _qkv(rng, B, Lq, Hq, Hkv, Lk=None, scale=1.0):
+    Lk = Lq if Lk is None else Lk
+    return randn(rng, B, Lq, Hq, 128, scale=scale), randn(rng, B, Lk, Hkv, 128), randn(rng, B, Lk, Hkv, 128)
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 8, 16, 48, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (7, 3), (64, 16), (100, 17), (300, 150)])
+def test_heads_windows_sinks(cuda_ok, G, window, sinks):
+    rng = np.random.default_rng(G + window + sinks)
+    n = 333 if G < 48 else 70
+    H = 2 if G < 48 else 1
+    _check(*_qkv(rng, 1, n, H * G, H), window, sinks)
+
+
+@pytest.mark.parametrize("Lq", [1, 2, 15, 16, 17, 64, 129])
+@pytest.mark.parametrize("off", [0, 1, 63, 1000])
+def test_lengths_and_offsets(cuda_ok, Lq, off):
+    rng = np.random.default_rng(Lq + off)
+    Q, K, V = _qkv(rng, 2, Lq, 4, 1, off + Lq)
+    for window, sinks in ((0, 0), (1, 1), (50, 4), (200, 70), (5000, 4)):
+        _check(Q, K, V, window, sinks, off)
+
+
+@pytest.mark.parametrize("window", [1, 16, 64, 128, 1000, 4096])
+def test_long(cuda_ok, window):
+    rng = np.random.default_rng(window)
+    Q, K, V = _qkv(rng, 1, 6000, 8, 1)
+    rows = np.unique(np.r_[0:3, 15:18, 127:130, rng.integers(0, 6000, 60), 5997:6000])
+    for sinks in (0, 4, 100):
+        _check(Q, K, V, window, sinks, rows=rows)
+
+
+def test_every_block_works_on_many_items(cuda_ok):
+    """More items than CTAs: ring, buffer and barrier phases carried from item to item, tile counts odd and even."""
+    rng = np.random.default_rng(77)
+    Q, K, V = _qkv(rng, 3, 1500, 16, 4)
+    rows = np.unique(rng.integers(0, 1500, 80))
+    for window, sinks in ((1, 0), (70, 0), (130, 4), (130, 20), (0, 0)):
+        a, la = _check(Q, K, V, window, sinks, rows=rows)
+        b, lb = rbs.swa_prefill(Q, K, V, window, sinks, return_lse=True)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("Lk,off", [(50, 0), (200, 100), (100, 200), (5, 300), (400, 0)])
+def test_keys_that_end_before_or_after_the_queries(cuda_ok, Lk, off):
+    """Keys past Lk do not exist; a query whose window lies past them sees the sinks or nothing (O 0, lse -inf)."""
+    rng = np.random.default_rng(Lk + off)
+    Q, K, V = _qkv(rng, 1, 150, 2, 1, Lk)
+    for window, sinks in ((40, 0), (40, 3), (40, 30), (0, 0), (1, 0)):
+        _check(Q, K, V, window, sinks, off)
+
+
+@pytest.mark.parametrize("scale,spread", [(2.0, 3.0), (1e-6, 1.0), (0.09, 20.0)])
+def test_score_sizes(cuda_ok, scale, spread):
+    rng = np.random.default_rng(31)
+    Q, K, V = _qkv(rng, 1, 500, 4, 2, scale=spread)
+    _check(Q, K, V, 150, 4, scale=scale)
+
+
+def test_rising_scores(cuda_ok):
+    """Keys whose scores rise along the sequence: every tile moves the maximum and scales the outputs."""
+    rng = np.random.default_rng(32)
+    Q, K, V = _qkv(rng, 1, 700, 2, 1)
+    d = f64(Q)[0, 0, 0]
+    K = torch.from_numpy((np.linspace(-4, 4, 700)[None, :, None, None] * d + 0.1 * f64(K)).astype(np.float32))
+    Q = torch.from_numpy((d + 0.1 * f64(Q)).astype(np.float32))
+    _check(Q.to(torch.bfloat16).cuda(), K.to(torch.bfloat16).cuda(), V, 300, 8, scale=0.5)
+
+
+def test_views_outputs_stream_graph(cuda_ok):
+    rng = np.random.default_rng(33)
+    qkv = randn(rng, 2, 200, 12, 128)
+    Q, K, V = qkv[:, :, :8], qkv[:, :, 8:10], qkv[:, :, 10:]
+    want, lse = _check(Q, K, V, 60, 4)
+    hold = torch.full((2, 8, 210, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        rbs.swa_prefill(Q, K, V, 60, 4, out=hold.transpose(1, 2)[:, 5:205])
+    s.synchronize()
+    assert torch.equal(hold.transpose(1, 2)[:, 5:205], want) and (hold[:, :, :5] == 7).all() and (hold[:, :, 205:] == 7).all()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, z = rbs.swa_prefill(Q, K, V, 60, 4, return_lse=True)
+    qkv.neg_()
+    qkv[:, 50:60] *= 2
+    g.replay()
+    a, b = rbs.swa_prefill(Q, K, V, 60, 4, return_lse=True)
+    assert torch.equal(o, a) and torch.equal(z, b)
+
+
+@pytest.mark.parametrize("G", [1, 4])
+def test_nan_and_infinity_in_masked_places(cuda_ok, G):
+    """NaN and infinite keys and values reach exactly the queries that see them; the others keep their results."""
+    rng = np.random.default_rng(34)
+    Q, K, V = _qkv(rng, 1, 400, 2 * G, 2)
+    want, wlse = rbs.swa_prefill(Q, K, V, 90, 5, return_lse=True)
+    K[0, 100, 0, 7] = float("nan")
+    V[0, 200, 0, 9] = float("inf")
+    V[0, 2, 1, 11] = float("nan")
+    V[0, 300, 1] = float("nan")
+    o, lse = rbs.swa_prefill(Q, K, V, 90, 5, return_lse=True)
+    see = S.visible(np.arange(400), np.arange(400), 90, 5)
+    off = 2 * BF16 * np.abs(f64(want)) + 2.0 ** -6  # the two ways round P differently
+    for h in range(2 * G):
+        k, v = f64(K)[0, :, h // G], f64(V)[0, :, h // G]
+        bad_k = (see & np.isnan(k).any(-1)[None]).any(1)
+        got = f64(o)[0, :, h]
+        assert np.isnan(got[bad_k]).all() and np.isnan(f64(lse)[0, h, bad_k]).all()
+        odd = (see[:, :, None] & ~np.isfinite(v)[None]).any(1) | bad_k[:, None]  # [token, dim]
+        assert np.array_equal(~np.isfinite(got), odd)
+        assert (np.abs(got - f64(want)[0, :, h])[~odd] <= off[0, :, h][~odd]).all()
+        assert np.array_equal(f64(lse)[0, h, ~bad_k], f64(wlse)[0, h, ~bad_k])

@@ -124,12 +124,33 @@ def test_attend(L):
     assert call(q=_fake(L=2, H=8, D=64)) == UNSUPPORTED
 
 
+def test_swa(L):
+    def call(q=None, k=None, v=None, o=None, window=4, sinks=1, off=0, scale=0.0, lse=None):
+        k = k or _fake(H=2, ptr=0x20000)
+        return L.swa_prefill(q or _fake(), k, v or k, window, sinks, off, scale, o or _fake(ptr=0x30000), lse, None)
+    assert call() == CUDA
+    assert call(window=0, sinks=0, off=77, scale=0.5, lse=0x9000) == CUDA
+    assert call(window=(1 << 31) - 1, sinks=(1 << 31) - 1) == CUDA
+    assert call(k=_fake(B=1, H=2)) == INVALID
+    assert call(v=_fake(L=7, H=2)) == INVALID
+    assert call(o=_fake(L=7)) == INVALID
+    assert call(k=_fake(H=3)) == INVALID
+    assert call(window=-1) == INVALID and call(sinks=-1) == INVALID and call(off=-1) == INVALID
+    assert call(scale=float("inf")) == INVALID
+    assert call(off=(1 << 31) - 8) == UNSUPPORTED
+    assert call(q=_fake(H=129), o=_fake(H=129), k=_fake(H=1)) == UNSUPPORTED
+    swapped = _abi.Bf16Tensor(0x20000, 2, 8, 2, 128, 2048, 128, 1024)  # heads outside tokens
+    assert call(k=swapped) == UNSUPPORTED
+
+
 def test_binding_refuses_host_tensors():
     q = torch.zeros(1, 2, 4, 128, dtype=torch.bfloat16)
     i = torch.zeros(1, 2, dtype=torch.int32)
     cache = rbs.KV4Cache(torch.zeros(3, 4, 2304, dtype=torch.uint8), 16)
     with pytest.raises(TypeError, match="CUDA"):
         rbs.rope_qk_norm(q, q, None, None, i, 1e4)
+    with pytest.raises(TypeError, match="CUDA"):
+        rbs.swa_prefill(q, q, q, 4)
     with pytest.raises(TypeError, match="CUDA"):
         rbs.kv4_append(cache, q, q, i)
     with pytest.raises(TypeError, match="CUDA"):
