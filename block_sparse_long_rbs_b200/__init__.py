@@ -355,9 +355,22 @@ def rope_reencode(x: torch.Tensor, old_pos: torch.Tensor, new_pos: torch.Tensor,
 # is taken as a raw handle.
 
 
+def _b(x, name: str) -> Bf16Tensor:
+    """_t with the passing case first."""
+    try:
+        if x.dtype is torch.bfloat16 and x.is_cuda:
+            B, L, H, D = x.shape
+            sb, ss, sh, sd = x.stride()
+            if sd == 1:
+                return Bf16Tensor(x.data_ptr(), B, L, H, D, sb, ss, sh)
+    except (AttributeError, ValueError):
+        pass
+    return _t(x, name)
+
+
 def _call(dev: torch.device, fn, where: str, *args) -> None:
     """fn(*args, stream) on dev's current stream."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
@@ -368,6 +381,8 @@ def _call(dev: torch.device, fn, where: str, *args) -> None:
 
 def _ints(x, name: str, dev: torch.device, *shape: int) -> int:
     """Device pointer of a contiguous int32 tensor of the given shape on dev."""
+    if isinstance(x, torch.Tensor) and x.dtype is torch.int32 and x.shape == shape and x.device == dev and x.is_contiguous():
+        return x.data_ptr()
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if x.dtype != torch.int32 or not x.is_contiguous():
@@ -398,10 +413,10 @@ def rope_qk_norm(Q: torch.Tensor, K: torch.Tensor, q_weight: torch.Tensor | None
     """Per-head norm of queries and keys and their rotation to pos ([L] or [B, L] int32), one pass.
     Returns (q_out, k_out); an output may be its input, for in place."""
     if q_out is None:
-        q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        q_out = torch.empty_like(Q)
     if k_out is None:
-        k_out = torch.empty(K.shape, dtype=K.dtype, device=K.device)
-    tq, tk, to, tp = _t(Q, "Q"), _t(K, "K"), _t(q_out, "q_out"), _t(k_out, "k_out")
+        k_out = torch.empty_like(K)
+    tq, tk, to, tp = _b(Q, "Q"), _b(K, "K"), _b(q_out, "q_out"), _b(k_out, "k_out")
     dev = Q.device
     if K.device != dev or q_out.device != dev or k_out.device != dev:
         _one_device("Q", Q, K=K, q_out=q_out, k_out=k_out)
@@ -427,13 +442,13 @@ def swa_prefill(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, window: int, 
                 softmax_scale: float | None = None, out: torch.Tensor | None = None, return_lse: bool = False):
     """Causal attention of Q [B, Lq, Hq, 128] over K, V [B, Lk, Hkv, 128] where the query at position p = t + q_offset
     sees the last `window` keys up to its own and the first `sinks` (window 0: every key up to its own)."""
-    tq, tk, tv = _t(Q, "Q"), _t(K, "K"), _t(V, "V")
+    tq, tk, tv = _b(Q, "Q"), _b(K, "K"), _b(V, "V")
     dev = Q.device
     if out is None:
-        out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        out = torch.empty_like(Q)
     B, Lq, Hq, D = Q.shape
-    lse = torch.empty(B, Hq, Lq, dtype=torch.float32, device=dev) if return_lse else None
-    to = _t(out, "out")
+    lse = Q.new_empty((B, Hq, Lq), dtype=torch.float32) if return_lse else None
+    to = _b(out, "out")
     if K.device != dev or V.device != dev or out.device != dev:
         _one_device("Q", Q, K=K, V=V, out=out)
     _call(dev, lib().swa_prefill, "swa_prefill", tq, tk, tv, window, sinks, q_offset,
@@ -489,11 +504,11 @@ def kv4_extend(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torc
     if max_new < 0:
         raise ValueError("max_new must be positive")
     if slots is None:
-        slots = torch.empty(B, max_new, dtype=torch.int32, device=dev)
+        slots = block_table.new_empty((B, max_new))
     if pos is None:
-        pos = torch.empty(B, max_new, dtype=torch.int32, device=dev)
+        pos = block_table.new_empty((B, max_new))
     if free_head_out is None:
-        free_head_out = torch.empty(1, dtype=torch.int32, device=dev)
+        free_head_out = block_table.new_empty((1,))
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise TypeError("free_pages: expected a contiguous int32 CUDA tensor [num_free]")
     n = free_pages.shape[0]
@@ -506,7 +521,7 @@ def kv4_extend(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torc
 
 def kv4_append(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor) -> None:
     """Quantise K and V [B, L, Hkv, 128] into the cache's slots [B, L] (int32; negative: padding, skipped)."""
-    tk, tv, c = _t(K, "K"), _t(V, "V"), cache.c()
+    tk, tv, c = _b(K, "K"), _b(V, "V"), cache.c()
     dev = K.device
     if V.device != dev or cache.data.device != dev:
         _one_device("K", K, V=V, cache=cache.data)
@@ -521,10 +536,10 @@ def kv4_load(cache: KV4Cache, slots: torch.Tensor, k_out: torch.Tensor | None = 
         raise TypeError("slots: expected a contiguous int32 CUDA tensor [B, L]")
     dev, shape = cache.data.device, (slots.shape[0], slots.shape[1], cache.data.shape[1], 128)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        k_out = slots.new_empty(shape, dtype=torch.bfloat16)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    tk, tv = _t(k_out, "k_out"), _t(v_out, "v_out")
+        v_out = torch.empty_like(k_out)
+    tk, tv = _b(k_out, "k_out"), _b(v_out, "v_out")
     if k_out.device != dev or v_out.device != dev:
         _one_device("cache", cache.data, k_out=k_out, v_out=v_out)
     _call(dev, lib().kv4_load, "kv4_load", c, _ints(slots, "slots", dev, k_out.shape[0], k_out.shape[1]), tk, tv)
@@ -542,16 +557,15 @@ def kv4_attend(Q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, lens
     """Attention of new tokens Q [B, Lq, Hq, 128] over the cached keys and values of their requests: query t of
     request b is at position starts[b] + t (lens[b] - Lq + t without starts) and sees the keys up to its own, with
     window > 0 only the last `window` of them and the first `sinks`."""
-    tq, c = _t(Q, "Q"), cache.c()
+    tq, c = _b(Q, "Q"), cache.c()
     dev = Q.device
     B, Lq, Hq, D = Q.shape
     if out is None:
-        out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
-    lse = torch.empty(B, Hq, Lq, dtype=torch.float32, device=dev) if return_lse else None
+        out = torch.empty_like(Q)
+    lse = Q.new_empty((B, Hq, Lq), dtype=torch.float32) if return_lse else None
     if workspace is None:
-        workspace = torch.empty(rbs_kv4_attend_workspace_bytes(Lq, Hq, cache.data.shape[1]), dtype=torch.uint8,
-                                device=dev)
-    to, w_ptr = _t(out, "out"), _dev(workspace, "workspace", torch.uint8)
+        workspace = Q.new_empty((rbs_kv4_attend_workspace_bytes(Lq, Hq, cache.data.shape[1]),), dtype=torch.uint8)
+    to, w_ptr = _b(out, "out"), _dev(workspace, "workspace", torch.uint8)
     if cache.data.device != dev or out.device != dev or workspace.device != dev:
         _one_device("Q", Q, cache=cache.data, out=out, workspace=workspace)
     t_ptr, stride, width = _table(block_table, "block_table", dev, B)

@@ -63,8 +63,13 @@ struct Kv4AttArgs {
   float v_scale;
   int tiles;  // row tiles of 8 NT rows per (request, KV head)
   float *part_o, *part_ml;  // workspace: two slots per CTA
-  int ctas;  // CTAs of the main kernel
+  int ctas;  // CTAs of the main kernel; those past the count of units have none
 };
+
+// CTAs that share the units: each has at least one.
+__device__ __forceinline__ int att_sharers(const Kv4AttArgs& a, int64_t total) {
+  return static_cast<int>(min(total, static_cast<int64_t>(a.ctas)));
+}
 
 // A request's visible range for its queries: sub-blocks [0, sink) and
 // [lo, hi), and the positions of its queries.
@@ -196,8 +201,9 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
     }
   const int HT = a.Hkv * a.tiles;
   const int64_t total = static_cast<int64_t>(prefix[a.B]) * HT;
-  int64_t u = total * blockIdx.x / a.ctas;
-  const int64_t u_end = total * (blockIdx.x + 1) / a.ctas;
+  const int sharers = att_sharers(a, total), me = min(static_cast<int>(blockIdx.x), sharers);
+  int64_t u = total * me / sharers;
+  const int64_t u_end = total * min(me + 1, sharers) / sharers;
   bool first_part = true;
 
   while (u < u_end) {
@@ -217,6 +223,41 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
     u += ub - ua;
     const AttRange rg = att_range(a, b);
     const int rows = a.G * a.Lq, row0 = tile * R;
+
+    // ---- sub-blocks v = 8 k + warp of units [ua, ub)
+    const int v_end = min(ub * kAttWarps, rg.n);
+    int v_load = ua * kAttWarps + warp;
+    auto real_sub = [&](int v) { return v < rg.sink ? v : v - rg.sink + rg.lo; };
+    auto page_of = [&](int sub) {
+      return a.spp_magic != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(sub), a.spp_magic)) : sub;
+    };
+    auto entry = [&](int v) -> int {
+      return v < v_end ? __ldg(a.table + b * a.table_b + page_of(real_sub(v))) : 0;
+    };
+    uint32_t taken = 0;  // bit per stage issued, newest lowest: its page was valid
+    int pg_next = entry(v_load);
+    int issued = 0;
+    auto issue = [&]() {
+      const bool any = v_load < v_end;
+      const bool ok = any && pg_next >= 0 && pg_next < a.num_pages;
+      if (any && !ok && lane == 0) raise_error(RBS_DEVERR_BLOCK_INDEX);
+      if (any) {
+        const int sub = real_sub(v_load), pgi = page_of(sub);
+        const uint8_t* src = a.data + ((static_cast<int64_t>(ok ? pg_next : 0) * a.Hkv + kvh) * a.spp + (sub - pgi * a.spp)) * kSubBytes;
+        const uint32_t dst = ring + (issued % kAttStages) * kSubBytes;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) cp_async16(dst + 512 * q + 16 * lane, src + 512 * q + 16 * lane, ok);
+        if (lane < 16) cp_async16(dst + 2048 + 16 * lane, src + 2048 + 16 * lane, ok);
+      }
+      cp_async_commit();
+      taken = (taken << 1) | (ok ? 1u : 0u);
+      ++issued;
+      v_load += kAttWarps;
+      pg_next = entry(v_load);
+    };
+#pragma unroll
+    for (int q = 0; q < kAttStages - 1; ++q) issue();
+
 
     // ---- Q fragments: row n of the tile, dims 16 s + {2j, 2j + 1, 2j + 8, 2j + 9}
     __syncthreads();  // the previous item's readers are done
@@ -270,40 +311,6 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
     const int t_lo = row0 / a.G, t_hi = (min(row0 + R, rows) - 1) / a.G;
     const int p_lo = rg.first_q + t_lo, p_hi = rg.first_q + t_hi;
     const bool all_live = p_lo >= 0 && p_hi < rg.len;
-
-    // ---- sub-blocks v = 8 k + warp of units [ua, ub)
-    const int v_end = min(ub * kAttWarps, rg.n);
-    int v_load = ua * kAttWarps + warp;
-    auto real_sub = [&](int v) { return v < rg.sink ? v : v - rg.sink + rg.lo; };
-    auto page_of = [&](int sub) {
-      return a.spp_magic != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(sub), a.spp_magic)) : sub;
-    };
-    auto entry = [&](int v) -> int {
-      return v < v_end ? __ldg(a.table + b * a.table_b + page_of(real_sub(v))) : 0;
-    };
-    uint32_t taken = 0;  // bit per stage issued, newest lowest: its page was valid
-    int pg_next = entry(v_load);
-    int issued = 0;
-    auto issue = [&]() {
-      const bool any = v_load < v_end;
-      const bool ok = any && pg_next >= 0 && pg_next < a.num_pages;
-      if (any && !ok && lane == 0) raise_error(RBS_DEVERR_BLOCK_INDEX);
-      if (any) {
-        const int sub = real_sub(v_load), pgi = page_of(sub);
-        const uint8_t* src = a.data + ((static_cast<int64_t>(ok ? pg_next : 0) * a.Hkv + kvh) * a.spp + (sub - pgi * a.spp)) * kSubBytes;
-        const uint32_t dst = ring + (issued % kAttStages) * kSubBytes;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) cp_async16(dst + 512 * q + 16 * lane, src + 512 * q + 16 * lane, ok);
-        if (lane < 16) cp_async16(dst + 2048 + 16 * lane, src + 2048 + 16 * lane, ok);
-      }
-      cp_async_commit();
-      taken = (taken << 1) | (ok ? 1u : 0u);
-      ++issued;
-      v_load += kAttWarps;
-      pg_next = entry(v_load);
-    };
-#pragma unroll
-    for (int q = 0; q < kAttStages - 1; ++q) issue();
 
     int done = 0;
     for (int v = ua * kAttWarps + warp; v < v_end; v += kAttWarps, ++done) {
@@ -540,48 +547,83 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
   asm volatile("griddepcontrol.launch_dependents;");
 }
 
-// Joins the parts of split items: one CTA per (request, KV head, row tile)
-// and row; thread = dim.  The CTAs whose runs meet the item follow from the
-// same prefix sums; their parts are added in order.
+// Joins the parts of split items: one CTA of four warps per (request, KV head,
+// row tile) and row.  The CTAs whose runs meet the item follow from the same
+// prefix sums.  The warps take the parts in turn, four dims a lane, and their
+// sums are added in warp order.
+constexpr int kAttMaxCtas = 2 * 160;
+
 template <int NT>
 __global__ void __launch_bounds__(128) kv4_combine_kernel(const __grid_constant__ Kv4AttArgs a) {
   constexpr int R = 8 * NT;
   __shared__ int64_t sums[4];
+  __shared__ float weight[kAttMaxCtas], red[8];
+  __shared__ float4 acc_s[4][32];
   extern __shared__ int32_t prefix[];
   const int HT = a.Hkv * a.tiles;
   const int item = blockIdx.x;  // b * HT + ht
   const int b = item / HT, ht = item - b * HT, kvh = ht / a.tiles, tile = ht - kvh * a.tiles;
   const int n = blockIdx.y, rows = a.G * a.Lq, row = tile * R + n;
-  // every block waits for the main kernel, so this grid never ends before it
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= rows) return;
   att_units(a, prefix, sums);
   const int64_t total = static_cast<int64_t>(prefix[a.B]) * HT;
+  const int sharers = att_sharers(a, total);
   const int nu = prefix[b + 1] - prefix[b];
   const int64_t u0 = static_cast<int64_t>(prefix[b]) * HT + static_cast<int64_t>(ht) * nu, u1 = u0 + nu;
-  // CTA c holds [total c / ctas, total (c + 1) / ctas): the one holding unit u is the last c with total c / ctas <= u
-  auto owner = [&](int64_t u) { return static_cast<int>(((u + 1) * a.ctas - 1) / total); };
-  const int c0 = owner(u0), c1 = owner(u1 - 1);
-  if (c0 == c1) return;  // whole in one CTA: written there
-  // the part is its CTA's first one unless the CTA's run began before the item
-  auto slot_of = [&](int c) { return 2 * c + (total * c / a.ctas < u0 ? 1 : 0); };
+  // CTA c holds [total c / sharers, total (c + 1) / sharers): unit u is with the last c whose run begins at or before it
+  const int c0 = static_cast<int>(((u0 + 1) * sharers - 1) / total), c1 = static_cast<int>((u1 * sharers - 1) / total);
+  // a part is its CTA's first one unless the CTA's run began before the item
+  const int first_slot = 2 * c0 + (total * c0 / sharers < u0 ? 1 : 0);
+  auto at = [&](int i) { return static_cast<int64_t>(i == 0 ? first_slot : 2 * (c0 + i)) * R + n; };
+  const int parts = c1 - c0 + 1;
+  // every block waits for the main kernel, so this grid never ends before it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row >= rows || parts == 1) return;  // one part: written by its CTA
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c) {
-    if (total * c / a.ctas >= total * (c + 1) / a.ctas) continue;  // a CTA with no units
-    m = fmaxf(m, a.part_ml[(static_cast<int64_t>(slot_of(c)) * R + n) * 2]);
-  }
-  float l = 0.f, acc = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    if (total * c / a.ctas >= total * (c + 1) / a.ctas) continue;
-    const int64_t at = static_cast<int64_t>(slot_of(c)) * R + n;
-    const float2 x = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+  for (int i = threadIdx.x; i < parts; i += 128) m = fmaxf(m, a.part_ml[at(i) * 2]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float l = 0.f;
+  for (int i = threadIdx.x; i < parts; i += 128) {
+    const float2 x = *reinterpret_cast<const float2*>(a.part_ml + at(i) * 2);
     const float f = x.x == -INFINITY ? 0.f : ptx_exp2(x.x - m);
+    weight[i] = f;
     l = fmaf(f, x.y, l);
-    acc = fmaf(f, a.part_o[at * 128 + threadIdx.x], acc);
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  if (lane == 0) red[4 + warp] = l;
+  __syncthreads();
+  l = (red[4] + red[5]) + (red[6] + red[7]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = warp; i < parts; i += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(a.part_o + at(i) * 128 + 4 * lane);
+    const float f = weight[i];
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  }
+  acc_s[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) {
+    const float4 x = acc_s[w][lane];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+  }
+  const float inv = l == 0.f ? 0.f : a.v_scale / l;
   const int t = row / a.G, h = kvh * a.G + row - t * a.G;
-  a.o[b * a.ob + t * a.os + h * a.oh + threadIdx.x] = __float2bfloat16(l == 0.f ? 0.f : acc * (a.v_scale / l));
-  if (a.lse != nullptr && threadIdx.x == 0)
+  *reinterpret_cast<uint2*>(a.o + b * a.ob + t * a.os + h * a.oh + 4 * lane) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (a.lse != nullptr && lane == 0)
     a.lse[(static_cast<int64_t>(b) * a.Hkv * a.G + h) * a.Lq + t] =
         l == 0.f ? -INFINITY : (m - kAttPShift + log2f(l)) * 0.69314718055994530942f;
 }

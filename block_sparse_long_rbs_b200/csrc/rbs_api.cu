@@ -1312,7 +1312,6 @@ rbs_status kv4_io(const rbs_kv4_cache* c, const rbs_bf16_tensor* K, const rbs_bf
 // 32 (the outputs of 32 rows fill half of a thread's registers).
 int attend_tiles_n(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 int attend_ctas(const DeviceInfo* di, int nt) { return di->sms * (nt <= 2 ? 2 : 1); }
-constexpr int kAttMaxCtas = 2 * 160;  // workspace sizes need no device
 
 }  // namespace
 
