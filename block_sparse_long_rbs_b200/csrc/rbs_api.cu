@@ -1160,15 +1160,20 @@ rbs_status rope_qk_norm(const rbs_bf16_tensor* q_in, rbs_bf16_tensor* q_out, con
 namespace {
 
 // 4-D map over [B, L, H, 128] bf16 with a box of 64 dims x `heads` heads x
-// `rows` tokens, 128-byte swizzle: rows ordered (token, head).
-rbs_status make_group_map(const rbs_bf16_tensor* t, int heads, int rows, CUtensorMap* map) {
+// `rows` tokens, 128-byte swizzle: rows ordered (token, head), or (head, token)
+// when the token stride is the smaller one (*seq_inner = 1).
+rbs_status make_group_map(const rbs_bf16_tensor* t, int heads, int rows, CUtensorMap* map, int* seq_inner) {
   PFN_encodeTiled enc = encode_fn();
   if (enc == nullptr) return fail(RBS_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
-  const cuuint64_t dims[4] = {RBS_HEAD_DIM, static_cast<cuuint64_t>(t->heads), static_cast<cuuint64_t>(t->seqlen),
+  const bool si = t->stride_s < t->stride_h;
+  *seq_inner = si ? 1 : 0;
+  const int64_t n[2] = {t->heads, t->seqlen}, s[2] = {t->stride_h, t->stride_s};
+  const int b[2] = {heads, rows};
+  const cuuint64_t dims[4] = {RBS_HEAD_DIM, static_cast<cuuint64_t>(n[si]), static_cast<cuuint64_t>(n[!si]),
                               static_cast<cuuint64_t>(t->batch)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(t->stride_h) * 2, static_cast<cuuint64_t>(t->stride_s) * 2,
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s[si]) * 2, static_cast<cuuint64_t>(s[!si]) * 2,
                                  static_cast<cuuint64_t>(t->stride_b) * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(b[si]), static_cast<cuuint32_t>(b[!si]), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1211,7 +1216,8 @@ rbs_status swa_prefill(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const
   DeviceInfo* di;
   if ((st = device_info(&di)) != RBS_OK) return st;
   int si;
-  if ((st = make_group_map(Q, static_cast<int>(G), a.T, &a.tmQ)) != RBS_OK) return st;
+  if ((st = make_group_map(Q, static_cast<int>(G), a.T, &a.tmQ, &si)) != RBS_OK) return st;
+  if ((st = make_group_map(O, static_cast<int>(G), a.T, &a.tmO, &a.o_seq_inner)) != RBS_OK) return st;
   for (int x = 0; x < 2; ++x) {
     const rbs_bf16_tensor* t = x == 0 ? K : V;
     if ((st = make_tensor_map(t, kWinKeys, x == 0 ? &a.tmK : &a.tmV, &si)) != RBS_OK) return st;
@@ -1237,6 +1243,8 @@ rbs_status swa_prefill(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const
   a.W = static_cast<int>(window == 0 ? end : std::min<int64_t>(window, end));
   a.S = static_cast<int>(std::min<int64_t>(sinks, end));
   a.items = static_cast<int>(items);
+  a.inv_nt = 1.f / static_cast<float>(a.nt);
+  a.inv_hkv = 1.f / static_cast<float>(a.Hkv);
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(RBS_HEAD_DIM));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = kWaitLimitNs;

@@ -19,11 +19,22 @@
 //              takes the maximum (the running maximum moves, and O is rescaled,
 //              only when it grows by more than 2^8), writes
 //              P = exp2(S c - m) as bf16 pairs over the scores, and at the end
-//              writes O / l and the LSE.
+//              stages O / l for a TMA store and writes the LSE.
 //   warp 4     Q and K producer, warp 5 V producer (TMA, one lane)
 //   warp 6     TMEM allocator, issuer of S = Q K^T (both operands in shared memory)
 //   warp 7     issuer of O += P V (P in TMEM, V MN-major in shared memory)
+//              and of the outputs' stores
 // TMEM columns: S buffers [0, 64) and [64, 128), O [128, 256).
+//
+// Bound by the softmax warps: per 64 scores of two rows a scheduler has 1024
+// cycles of exponentials (16 a clock and SM), and the two warps that share it
+// overlap them with only part of their other work (1890 cycles per pair of
+// tiles measured; the products need 1280: 48 cycles per K = 16 step of S at
+// N = 64, where shared memory is the limit, and 64 of P V).  Measured and left,
+// 16,384 tokens, window 4096, 32 q / 4 KV heads, 892 us as here: one CTA with two
+// row tiles on shared key tiles (1056 us: the two run in step, and their
+// exponentials collide), key tiles of 128 in that form (1120 us), a quarter of
+// the exponentials as a polynomial (915 us).
 //
 // Masked scores are replaced before the softmax, so NaN keys stay out; a NaN or
 // infinite value in a masked place still meets a zero weight in the product.
@@ -37,16 +48,18 @@
 namespace rbs {
 
 struct WinArgs {
-  // Q boxes of T tokens x G heads, K / V boxes of 64, 16 and 48 keys
-  CUtensorMap tmQ, tmK, tmV, tmKs, tmVs, tmKw, tmVw;
+  // Q boxes of T tokens x G heads, O's the same (ordered by stride), K / V boxes of 64, 16 and 48 keys
+  CUtensorMap tmQ, tmO, tmK, tmV, tmKs, tmVs, tmKw, tmVw;
   const __nv_bfloat16 *Q, *K, *V;
   __nv_bfloat16* O;
   int64_t qb, qs, qh, kb, ks, kh, vb, vs, vh, ob, os, oh;
+  int o_seq_inner;  // O's token stride is the smaller one: its box is T tokens inside G heads
   float* lse;  // [B, Hq, Lq] or null
   int B, G, Hkv, Lq, Lk, T, nt;  // T tokens per item, nt items per (batch, KV head)
   int64_t q_off;
   int W, S;
   int items;
+  float inv_nt, inv_hkv;
   float scale_log2;
   uint64_t wait_ns;
 };
@@ -62,9 +75,11 @@ struct WinSmem {
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + kQBytes;
   static constexpr int kV = kK + kWinNS * kKVBytes;
-  static constexpr int kBar = kV + kWinNS * kKVBytes;
-  static constexpr int kTotal = kBar + 256;
-  static constexpr int kAlloc = kTotal + 1024;
+  static constexpr int kO = kV + kWinNS * kKVBytes;  // 64 dims of the outputs, on their way to the store
+  static constexpr int kBar = kO + 128 * 128;
+  // no slack for alignment: the block's dynamic shared memory starts at a
+  // multiple of 1024 (checked)
+  static constexpr int kAlloc = kBar + 256;
   static constexpr uint32_t kTmemCols = 256;
   __host__ __device__ static constexpr uint32_t col_s(int buf) { return buf * kWinKeys; }
   static constexpr uint32_t kColO = 128;
@@ -81,7 +96,9 @@ enum : int {
   kWbPVDone = kWbPFull + 2,      // + tile mod 4
   kWbOFull = kWbPVDone + 4,
   kWbOEmpty = kWbOFull + 1,
-  kWbDrain = kWbOEmpty + 1,      // + issuer
+  kWbStoreFull = kWbOEmpty + 1,  // 64 dims of the outputs are staged
+  kWbStoreEmpty = kWbStoreFull + 1,
+  kWbDrain = kWbStoreEmpty + 1,  // + issuer
   kWbNum = kWbDrain + 2
 };
 static_assert(kWbNum * 8 + 16 <= 256, "barrier area");
@@ -98,13 +115,22 @@ struct WinItem {
   int n;               // tiles
 };
 
+// n / d by the reciprocal and a correction; the quotient is off by one at most
+// while it stays below 2^22, and the loops mend any other.
+__device__ __forceinline__ int win_div(int n, int d, float inv, int& rem) {
+  int q = static_cast<int>(static_cast<float>(n) * inv);
+  rem = n - q * d;
+  while (rem < 0) { --q; rem += d; }
+  while (rem >= d) { ++q; rem -= d; }
+  return q;
+}
+
 __device__ __forceinline__ WinItem win_item(const WinArgs& a, int w) {
   WinItem x;
-  const int per_b = a.Hkv * a.nt;
-  x.b = w / per_b;
-  const int rem = w - x.b * per_b;
-  x.kvh = rem / a.nt;
-  x.t0 = (a.nt - 1 - (rem - x.kvh * a.nt)) * a.T;  // the last tokens, with the most keys, first
+  int i;
+  const int bh = win_div(w, a.nt, a.inv_nt, i);
+  x.b = win_div(bh, a.Hkv, a.inv_hkv, x.kvh);
+  x.t0 = (a.nt - 1 - i) * a.T;  // the last tokens, with the most keys, first
   x.p0 = static_cast<int>(a.q_off) + x.t0;
   x.p1 = min(x.p0 + a.T, static_cast<int>(a.q_off) + a.Lq) - 1;
   const int hi = min(x.p1, a.Lk - 1);
@@ -124,9 +150,9 @@ __device__ __forceinline__ int win_key0(const WinItem& x, int t) {
   return x.lo - (x.merged ? kWinSinkRows : 0) + (t - x.n_sink) * kWinKeys;
 }
 
-// One row from the visible keys alone, by a whole warp: lane l holds dims
-// 4l .. 4l + 3.  Only rows whose fast result is not finite come here.
-__device__ __noinline__ void window_exact_row(const WinArgs& a, int b, int kvh, int h, int t) {
+// One row from the visible keys alone, by a whole warp: lane l holds and
+// returns dims 4l .. 4l + 3.  Only rows whose fast result is not finite come here.
+__device__ __noinline__ uint2 window_exact_row(const WinArgs& a, int b, int kvh, int h, int t) {
   const int lane = threadIdx.x & 31;
   const int p = static_cast<int>(a.q_off) + t, w0 = max(0, p - a.W + 1), hi = min(p, a.Lk - 1);
   const uint2 qx = *reinterpret_cast<const uint2*>(a.Q + b * a.qb + t * a.qs + h * a.qh + 4 * lane);
@@ -149,15 +175,18 @@ __device__ __noinline__ void window_exact_row(const WinArgs& a, int b, int kvh, 
   for (int s = 0; s < min(min(a.S, w0), a.Lk); ++s) take(s);
   for (int s = w0; s <= hi; ++s) take(s);
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(a.O + b * a.ob + t * a.os + h * a.oh + 4 * lane) =
-      make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  return make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
 }
 
 __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __grid_constant__ WinArgs a) {
   using L = WinSmem;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw;
   const uint32_t sbase = smem_u32(smem);
+  if ((sbase & 1023u) != 0) {  // the swizzled tiles would not be where the products look
+    if (threadIdx.x == 0) raise_error(RBS_DEVERR_TIMEOUT);
+    return;
+  }
   const uint32_t sQ = sbase + L::kQ, sK = sbase + L::kK, sV = sbase + L::kV, bars = sbase + L::kBar;
   auto bar = [&](int k) -> uint32_t { return bars + 8u * k; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBar + kWbNum * 8);
@@ -179,6 +208,8 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
     for (int s = 0; s < 4; ++s) mbar_init(bar(kWbPVDone + s), 1);
     mbar_init(bar(kWbOFull), 1);
     mbar_init(bar(kWbOEmpty), 4);
+    mbar_init(bar(kWbStoreFull), 4);
+    mbar_init(bar(kWbStoreEmpty), 1);
     mbar_init(bar(kWbDrain), 1);
     mbar_init(bar(kWbDrain + 1), 1);
     *abort_flag = 0;
@@ -298,6 +329,20 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
           if (t == x.n - 1) umma_commit_warp(bar(kWbOFull));
         }
       }
+      if (!isS && ok) {
+        // the outputs' stores: the softmax warps stage them while this warp has
+        // nothing to issue, the next item's first weights coming after them
+        for (int hf = 0; hf < 2 && ok; ++hf) {
+          if (!wait(kWbStoreFull, hf)) { ok = false; break; }  // two phases per item
+          if (lane == 0) {
+            tma_store_4d(&a.tmO, sbase + L::kO, 64 * hf, a.o_seq_inner ? x.t0 : x.kvh * a.G, a.o_seq_inner ? x.kvh * a.G : x.t0, x.b);
+            tma_store_commit();
+            tma_store_wait_read();
+            mbar_arrive(bar(kWbStoreEmpty));
+          }
+          __syncwarp();
+        }
+      }
       ++it;
     }
     // drain this issuer's tensor-core work before TMEM is freed
@@ -313,16 +358,16 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(k));
     };
-    uint32_t g = 0, it = 0;
+    uint32_t g = 0, it = 0, ns = 0;  // tiles, items, halves of outputs staged
     bool ok = true;
     for (int w = blockIdx.x; w < a.items && ok; w += gridDim.x) {
       const WinItem x = win_item(a, w);
       const int t_row = x.t0 + tl, h = x.kvh * a.G + gh;
       const bool live = tl < a.T && t_row < a.Lq;
       const int64_t lse_at = (static_cast<int64_t>(x.b) * a.G * a.Hkv + h) * a.Lq + t_row;
-      uint4* dst = reinterpret_cast<uint4*>(a.O + x.b * a.ob + t_row * a.os + h * a.oh);
       if (x.n == 0) {
         if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.O + x.b * a.ob + t_row * a.os + h * a.oh);
           for (int k = 0; k < 16; ++k) dst[k] = make_uint4(0, 0, 0, 0);
           if (a.lse != nullptr) a.lse[lse_at] = -INFINITY;
         }
@@ -343,18 +388,24 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
         const int k0 = win_key0(x, t);
         const bool sink_tile = t < x.n_sink, shared = t == 0 && x.merged;
         if (sink_tile || shared || k0 + kWinKeys - 1 > min(x.p0, a.Lk - 1) || k0 <= x.p1 - a.W) {
-          // column e is hidden above hi_c, and below lo_c unless it is a sink
+          // columns are seen up to hi_c from lo_c on, and below sk_c (sinks): a bit per column
           const int hi_c = hi - k0, lo_c = sink_tile ? kWinKeys : w_lo - k0;
           const int sk_c = sink_tile ? x.sinks - k0 : shared ? x.sinks : a.S - k0;
+          auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };  // columns 0 .. n - 1
+          const unsigned long long see = below(hi_c + 1) & (~below(lo_c) | below(sk_c));
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e > hi_c || (e < lo_c && e >= sk_c)) v[e >> 5][e & 31] = __float_as_uint(-INFINITY);
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t bits = static_cast<uint32_t>(see >> (32 * q));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(bits & (1u << e))) v[q][e] = __float_as_uint(-INFINITY);
+          }
         }
-        float mx = -INFINITY;
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) mx = fmax3(mx, __uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1]));
+        for (int e = 0; e < 64; e += 2)
+          m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1]));
+        const float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
         const float m_new = fmaxf(m_used, mx * c);
         float factor = 1.f;
         bool rescale = false;
@@ -410,34 +461,53 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (!__all_sync(0xffffffffu, mbar_wait(bar(kWbOFull), it & 1, abort_flag, limit))) { ok = false; break; }
       tc_fence_after();
-      float odd = 0.f;  // stays 0 while every output is finite
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      float2 sum = make_float2(0.f, 0.f);  // finite while every output is
+      const float2 inv2 = make_float2(inv, inv);
+      // this row in the store's box (128-byte swizzle: 16-byte chunk k of row r at k ^ (r % 8))
+      const int ro = a.o_seq_inner ? gh * a.T + tl : r;
+      uint32_t ow[2][32];  // the row as bf16 pairs
+      {
         uint32_t o[32];
-        tmem_ld32(lane_base + L::kColO + 32 * q, o);
-        tmem_wait_ld();
-        if (q == 3) {
-          tc_fence_before();
-          warp_arrive(kWbOEmpty);
-        }
-        float f[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          f[e] = __uint_as_float(o[e]) * inv;
-          odd = fmaf(f[e], 0.f, odd);
-        }
-        if (live) {
+        for (int q = 0; q < 4; ++q) {
+          tmem_ld32(lane_base + L::kColO + 32 * q, o);
+          tmem_wait_ld();
+          if (q == 3) {
+            tc_fence_before();
+            warp_arrive(kWbOEmpty);
+          }
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            __stcs(dst + 4 * q + k, make_uint4(pack_bf16x2(f[8 * k], f[8 * k + 1]), pack_bf16x2(f[8 * k + 2], f[8 * k + 3]),
-                                               pack_bf16x2(f[8 * k + 4], f[8 * k + 5]), pack_bf16x2(f[8 * k + 6], f[8 * k + 7])));
+          for (int e = 0; e < 16; ++e) {
+            const float2 f2 = fmul2(make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2);
+            sum = fadd2(sum, f2);
+            ow[q >> 1][16 * (q & 1) + e] = pack_bf16x2(f2.x, f2.y);
+          }
         }
       }
       if (live && a.lse != nullptr) a.lse[lse_at] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f;
-      for (uint32_t bad = __ballot_sync(0xffffffffu, live && odd != 0.f); bad != 0; bad &= bad - 1) {
+      const bool odd = live && !(fabsf(sum.x + sum.y) < INFINITY);
+      for (uint32_t bad = __ballot_sync(0xffffffffu, odd); bad != 0; bad &= bad - 1) {
         const int src = __ffs(bad) - 1;
-        __syncwarp();
-        window_exact_row(a, x.b, x.kvh, __shfl_sync(0xffffffffu, h, src), __shfl_sync(0xffffffffu, t_row, src));
+        const uint2 y = window_exact_row(a, x.b, x.kvh, __shfl_sync(0xffffffffu, h, src), __shfl_sync(0xffffffffu, t_row, src));
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {  // pair e is in lane e / 2
+          const uint32_t z = __shfl_sync(0xffffffffu, (e & 1) ? y.y : y.x, e >> 1);
+          if (lane == src) ow[e >> 5][e & 31] = z;
+        }
+      }
+      // 64 dims at a time through the staging buffer, whose stores warp 7 issues
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf, ++ns) {
+        if (ns >= 1 && !__all_sync(0xffffffffu, mbar_wait(bar(kWbStoreEmpty), (ns - 1) & 1, abort_flag, limit))) { ok = false; break; }
+        if (tl < a.T) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sbase + L::kO + ro * 128 + ((k ^ (ro & 7)) << 4)),
+                         "r"(ow[hf][4 * k]), "r"(ow[hf][4 * k + 1]), "r"(ow[hf][4 * k + 2]), "r"(ow[hf][4 * k + 3])
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+        warp_arrive(kWbStoreFull);
       }
       ++it;
     }
