@@ -15,7 +15,8 @@
 // kv4_combine_kernel joins them in their order, so results do not vary.
 //
 // A warp works on its own sub-blocks with no barrier: 2304 bytes by 16-byte
-// asynchronous copies into its ring, then
+// asynchronous copies into its ring, then, the first product of a sub-block
+// beside the second one of the sub-block before,
 //   S^T (16 keys x 8 rows) = K Q^T,  O^T (16 dims x 8 rows) += V^T P^T
 // by mma.m16n8k16 in fp16 with fp32 sums: rows of queries are the instruction's
 // narrow side, since one token's G rows rarely fill the wide one.  The codes
@@ -40,14 +41,16 @@ namespace rbs {
 
 constexpr int kAttWarps = 8;
 constexpr int kAttThreads = kAttWarps * 32;
-constexpr int kAttStages = 4;
+constexpr int kAttStages = 5;
 constexpr int kAttMaxBatch = 4096;
 constexpr float kAttPShift = 6.f;  // P carries 2^6
+constexpr float kAttNoMax = -1e30f;  // the running maximum of a row that has seen no key
 
 struct Kv4AttArgs {
   const uint8_t* data;
   int64_t num_pages;
   int Hkv, G, page, spp;      // spp: sub-blocks per page
+  uint32_t page_bytes;        // of all heads: at most 65535 * 16 * 2304
   uint32_t spp_magic;         // ceil(2^32 / spp); 0 when spp is 1
   const int32_t* table;
   int64_t table_b;
@@ -126,6 +129,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -150,8 +160,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t dup_lo(uint32_t x) { return __byte_perm(x, x, 0x1010); }
-__device__ __forceinline__ uint32_t dup_hi(uint32_t x) { return __byte_perm(x, x, 0x3232); }
+// a times either half of s
+__device__ __forceinline__ uint32_t hmul2_half(uint32_t a, uint32_t s, int hi) {
+  const __half2 x = *reinterpret_cast<const __half2*>(&a), y = *reinterpret_cast<const __half2*>(&s);
+  const __half2 r = __hmul2(x, hi ? __high2half2(y) : __low2half2(y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -172,21 +186,22 @@ struct AttSmem {
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kAttWarps * kAttStages * kSubBytes;  // Q fragments [8 groups][NT][32 lanes][8 B]
   static constexpr int kQExp = kQ + 8 * NT * 256;                        // float [8 NT]: the rows' powers of two
-  static constexpr int kMerge = kQExp + 8 * NT * 4;                      // float [8 warps][8 rows][128 + 4]
-  static constexpr int kML = kMerge + kAttWarps * 8 * 132 * 4;           // float [8 warps][8 NT][2]
+  // a warp's part for joining, float [8 rows][128 + 4], lies over its own ring
+  static_assert(kAttStages * kSubBytes >= 8 * 132 * 4, "the ring holds it");
+  static constexpr int kML = kQExp + 8 * NT * 4;                         // float [8 warps][8 NT][2]
   static constexpr int kSums = kML + kAttWarps * 8 * NT * 8;             // int64 [warps]
   static constexpr int kPrefix = kSums + kAttWarps * 8;                  // int32 [B + 1]
   static constexpr int bytes(int B) { return kPrefix + (B + 1) * 4; }
 };
 
-template <int NT>
+// ONE: every request has one query token (Lq == 1).
+template <int NT, bool ONE>
 __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kernel(const __grid_constant__ Kv4AttArgs a) {
   using L = AttSmem<NT>;
   constexpr int R = 8 * NT;  // rows of a tile
   extern __shared__ __align__(16) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   float* qexp = reinterpret_cast<float*>(smem + L::kQExp);
-  float* merge = reinterpret_cast<float*>(smem + L::kMerge);
   float* ml = reinterpret_cast<float*>(smem + L::kML);
   int64_t* sums = reinterpret_cast<int64_t*>(smem + L::kSums);
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefix);
@@ -226,41 +241,45 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
 
     // ---- sub-blocks v = 8 k + warp of units [ua, ub)
     const int v_end = min(ub * kAttWarps, rg.n);
-    int v_load = ua * kAttWarps + warp;
-    auto real_sub = [&](int v) { return v < rg.sink ? v : v - rg.sink + rg.lo; };
-    auto page_of = [&](int sub) {
-      return a.spp_magic != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(sub), a.spp_magic)) : sub;
+    const int shift = rg.lo - rg.sink;  // from a sub-block's place in the item to its place in the request, past the sinks
+    const int32_t* table = a.table + b * a.table_b;
+    const uint8_t* head_data = a.data + static_cast<int64_t>(kvh) * a.spp * kSubBytes + 16 * lane;
+    const uint32_t ring_lane = ring + 16 * lane;
+    // the next sub-block to load: its table entry is fetched one step ahead
+    int v_load = ua * kAttWarps + warp, pg_next = 0;
+    uint32_t off_next = 0, dst_next = ring_lane;
+    auto look = [&]() {
+      if (v_load < v_end) {
+        const int sub = v_load < rg.sink ? v_load : v_load + shift;
+        const int pi = a.spp_magic != 0 ? static_cast<int>(__umulhi(static_cast<uint32_t>(sub), a.spp_magic)) : sub;
+        pg_next = __ldg(table + pi);
+        off_next = static_cast<uint32_t>(sub - pi * a.spp) * kSubBytes;
+      }
     };
-    auto entry = [&](int v) -> int {
-      return v < v_end ? __ldg(a.table + b * a.table_b + page_of(real_sub(v))) : 0;
-    };
+    look();
     uint32_t taken = 0;  // bit per stage issued, newest lowest: its page was valid
-    int pg_next = entry(v_load);
-    int issued = 0;
     auto issue = [&]() {
-      const bool any = v_load < v_end;
-      const bool ok = any && pg_next >= 0 && pg_next < a.num_pages;
-      if (any && !ok && lane == 0) raise_error(RBS_DEVERR_BLOCK_INDEX);
-      if (any) {
-        const int sub = real_sub(v_load), pgi = page_of(sub);
-        const uint8_t* src = a.data + ((static_cast<int64_t>(ok ? pg_next : 0) * a.Hkv + kvh) * a.spp + (sub - pgi * a.spp)) * kSubBytes;
-        const uint32_t dst = ring + (issued % kAttStages) * kSubBytes;
+      bool ok = false;
+      if (v_load < v_end) {
+        ok = static_cast<uint32_t>(pg_next) < static_cast<uint32_t>(a.num_pages);
+        if (!ok && lane == 0) raise_error(RBS_DEVERR_BLOCK_INDEX);
+        const uint8_t* src = head_data + (static_cast<uint64_t>(ok ? static_cast<uint32_t>(pg_next) : 0u) * a.page_bytes + off_next);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) cp_async16(dst + 512 * q + 16 * lane, src + 512 * q + 16 * lane, ok);
-        if (lane < 16) cp_async16(dst + 2048 + 16 * lane, src + 2048 + 16 * lane, ok);
+        for (int q = 0; q < 4; ++q) cp_async16(dst_next + 512 * q, src + 512 * q, ok);
+        if (lane < 16) cp_async16(dst_next + 2048, src + 2048, ok);
       }
       cp_async_commit();
       taken = (taken << 1) | (ok ? 1u : 0u);
-      ++issued;
+      dst_next = dst_next == ring_lane + (kAttStages - 1) * kSubBytes ? ring_lane : dst_next + kSubBytes;
       v_load += kAttWarps;
-      pg_next = entry(v_load);
+      look();
     };
+    __syncthreads();  // the previous item's readers are done
 #pragma unroll
     for (int q = 0; q < kAttStages - 1; ++q) issue();
 
 
     // ---- Q fragments: row n of the tile, dims 16 s + {2j, 2j + 1, 2j + 8, 2j + 9}
-    __syncthreads();  // the previous item's readers are done
     for (int n = warp; n < R; n += kAttWarps) {
       const int row = row0 + n;
       uint2 x = make_uint2(0, 0);
@@ -298,7 +317,7 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
         sc[nt][i] = a.scale_log2 * qexp[n];
         const int p = row < rows ? rg.first_q + row / a.G : -1;
         qp[nt][i] = p < rg.len ? p : -1;  // -1: the row sees nothing
-        m_run[nt][i] = -INFINITY;
+        m_run[nt][i] = kAttNoMax;
         l_run[nt][i] = 0.f;
       }
 #pragma unroll
@@ -311,58 +330,51 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
     const int t_lo = row0 / a.G, t_hi = (min(row0 + R, rows) - 1) / a.G;
     const int p_lo = rg.first_q + t_lo, p_hi = rg.first_q + t_hi;
     const bool all_live = p_lo >= 0 && p_hi < rg.len;
+    // sub-blocks that every row sees whole: below full_sink, and in [full_lo, full_hi)
+    const int full_hi = all_live ? ((p_lo + 1) >> 4) - shift : 0;
+    const int full_lo = a.window == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(max(p_hi - a.window + 1, 0)) + 15u) >> 4) - shift;
+    const int full_sink = all_live ? min(rg.sink, a.sinks >> 4) : 0;
 
-    int done = 0;
-    for (int v = ua * kAttWarps + warp; v < v_end; v += kAttWarps, ++done) {
-      cp_async_wait<kAttStages - 2>();
-      __syncwarp();  // every lane's copies have landed, and the stage issued next is read out
-      issue();
-      const uint32_t st = ring + (done % kAttStages) * kSubBytes;
-      const bool valid = (taken >> (kAttStages - 1)) & 1u;
-      const int tok0 = real_sub(v) * 16;
-      // fully visible to every row of the tile
-      const bool full = valid && all_live && tok0 + 15 <= p_lo &&
-                        (a.window == 0 || tok0 > p_hi - a.window || tok0 + 15 < a.sinks);
-      // ---- S^T = K Q^T
+    // ---- the sub-blocks: scores of the next one beside the products of this one
+    uint32_t p0[NT], p1[NT];  // P^T, the second product's operand: keys 2j, 2j + 1 (+ 8) of row r
+    bool full = true, valid = true;  // of the sub-block whose P these are
+    int tok0 = 0;
+
+    // S^T = K Q^T of a stage, unscaled
+    auto scores = [&](uint32_t st, float (&c)[NT][4]) {
       const uint4 ka = lds128(st + 16 * lane), kb = lds128(st + 512 + 16 * lane);
       const uint2 sa = lds64(st + 2048 + 8 * r), sbk = lds64(st + 2048 + 64 + 8 * r);
-      float c[NT][4];
+      uint32_t fa[4], fb[4];  // f16x2 scales of groups (0,1), (2,3), ...
+      e4m3x4_f16(sa.x, fa[0], fa[1]);
+      e4m3x4_f16(sa.y, fa[2], fa[3]);
+      e4m3x4_f16(sbk.x, fb[0], fb[1]);
+      e4m3x4_f16(sbk.y, fb[2], fb[3]);
+      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int w = 0; w < 4; ++w) {
+        uint32_t xa[4], xb[4];
+        e2m1x8_f16(wa[w], xa);
+        e2m1x8_f16(wb[w], xb);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) c[nt][q] = 0.f;
-      {
-        uint32_t fa[4], fb[4];  // f16x2 scales of groups (0,1), (2,3), ...
-        e4m3x4_f16(sa.x, fa[0], fa[1]);
-        e4m3x4_f16(sa.y, fa[2], fa[3]);
-        e4m3x4_f16(sbk.x, fb[0], fb[1]);
-        e4m3x4_f16(sbk.y, fb[2], fb[3]);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        for (int e = 0; e < 2; ++e) {
+          const int s = 2 * w + e;
+          const uint32_t a0 = hmul2_half(xa[2 * e], fa[w], e), a1 = hmul2_half(xb[2 * e], fb[w], e);
+          const uint32_t a2 = hmul2_half(xa[2 * e + 1], fa[w], e), a3 = hmul2_half(xb[2 * e + 1], fb[w], e);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t xa[4], xb[4];
-          e2m1x8_f16(wa[w], xa);
-          e2m1x8_f16(wb[w], xb);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int s = 2 * w + e;
-            const uint32_t ga = e == 0 ? dup_lo(fa[w]) : dup_hi(fa[w]), gb = e == 0 ? dup_lo(fb[w]) : dup_hi(fb[w]);
-            const uint32_t a0 = hmul2(xa[2 * e], ga), a1 = hmul2(xb[2 * e], gb);
-            const uint32_t a2 = hmul2(xa[2 * e + 1], ga), a3 = hmul2(xb[2 * e + 1], gb);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 qf = lds64(sb + L::kQ + ((s * NT + nt) * 32 + lane) * 8);
-              mma_f16(c[nt], a0, a1, a2, a3, qf.x, qf.y);
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 qf = lds64(sb + L::kQ + ((s * NT + nt) * 32 + lane) * 8);
+            if (s == 0) mma_f16_first(c[nt], a0, a1, a2, a3, qf.x, qf.y);
+            else mma_f16(c[nt], a0, a1, a2, a3, qf.x, qf.y);
           }
         }
       }
-      // ---- scores in log2 units, masked; c[nt][2 i + q]: key r + 8 i, row column q
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) c[nt][q] *= sc[nt][q & 1];
+    };
+    // scores -> P of sub-block v, whose page was there or not; c[nt][2 i + q]: key r + 8 i, row column q
+    auto weights = [&](float (&c)[NT][4], int v, bool there) {
+      valid = there;
+      full = there && (v < full_sink || (v >= full_lo && v < full_hi));
       if (!full) {
+        tok0 = (v < rg.sink ? v : v + shift) * 16;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -372,12 +384,15 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
             if (!see) c[nt][q] = -INFINITY;
           }
       }
-      // ---- running maximum, moved only when a score passes it by 2^8
+      // exponents of P; the running maximum moves only when a score passes it by 2^8
+      float e[NT][4];
       bool up = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) up = up || fmaxf(c[nt][i], c[nt][2 + i]) > m_run[nt][i] + 8.f;
+        for (int q = 0; q < 4; ++q) e[nt][q] = fmaf(c[nt][q], sc[nt][q & 1], kAttPShift - m_run[nt][q & 1]);
+        up = up || fmaxf(fmax3(e[nt][0], e[nt][1], e[nt][2]), e[nt][3]) > 8.f + kAttPShift;
+      }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -387,8 +402,8 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = fmaxf(m_run[nt][i], mx);
-            const float f = m_run[nt][i] == -INFINITY ? 0.f : ptx_exp2(m_run[nt][i] - mn);
+            const float mn = fmaxf(m_run[nt][i], mx * sc[nt][i]);
+            const float f = ptx_exp2(m_run[nt][i] - mn);
             m_run[nt][i] = mn;
             l_run[nt][i] *= f;
 #pragma unroll
@@ -396,89 +411,113 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
               o[s][nt][i] *= f;
               o[s][nt][2 + i] *= f;
             }
+            e[nt][i] = fmaf(c[nt][i], sc[nt][i], kAttPShift - mn);
+            e[nt][2 + i] = fmaf(c[nt][2 + i], sc[nt][i], kAttPShift - mn);
           }
       }
-      // ---- P^T as the second product's operand: keys 2j, 2j + 1 (+ 8) of row r
-      uint32_t p0[NT], p1[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float e[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float m = m_run[nt][q & 1] == -INFINITY ? 0.f : m_run[nt][q & 1];
-          e[q] = ptx_exp2(c[nt][q] - m + kAttPShift);
-        }
-        l_run[nt][0] += e[0] + e[2];
-        l_run[nt][1] += e[1] + e[3];
-        p0[nt] = movmatrix_trans(pack_f16x2(e[0], e[1]));
-        p1[nt] = movmatrix_trans(pack_f16x2(e[2], e[3]));
+        for (int q = 0; q < 4; ++q) e[nt][q] = ptx_exp2(e[nt][q]);
+        l_run[nt][0] += e[nt][0] + e[nt][2];
+        l_run[nt][1] += e[nt][1] + e[nt][3];
+        p0[nt] = movmatrix_trans(pack_f16x2(e[nt][0], e[nt][1]));
+        p1[nt] = movmatrix_trans(pack_f16x2(e[nt][2], e[nt][3]));
       }
-      // ---- O^T += V^T P^T; group s is dims 16 s .. 16 s + 15 of the instruction's 16 rows
+    };
+    // which of keys k0, k0 + 1 of the sub-block the query at position pt sees, as a mask of scale bytes
+    auto keep = [&](int k0, int pt) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = tok0 + k0 + i;
+        if (valid && pt < rg.len && key <= pt && (a.window == 0 || key > pt - a.window || key < a.sinks)) m |= 0x00ff00ffu << (8 * i);
+      }
+      return m;
+    };
+    // O^T += V^T P^T of a stage; group s is dims 16 s .. 16 s + 15 of the
+    // instruction's 16 rows.  All columns, or (part) those of token t alone:
+    // 0 times a NaN value is one, so other columns are left out and not given
+    // zero weights.
+    auto product = [&](auto part, uint32_t st, const uint4& ta, const uint4& tb, int t) {
+      bool mine[NT][2];
+      if (part)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) mine[nt][i] = (row0 + 8 * nt + 2 * j + i) / a.G == t;
       const uint4 va = lds128(st + 1024 + 16 * lane), vb = lds128(st + 1536 + 16 * lane);
-      const uint4 ta = lds128(st + 2176 + 16 * j), tb = lds128(st + 2176 + 64 + 16 * j);
-      // all columns, or (part) the columns of token t alone: 0 times a NaN
-      // value is one, so other columns are left out and not given zero weights
-      auto product = [&](auto part, uint32_t keep_a, uint32_t keep_b, int t) {
-        bool mine[NT][2];
-        if (part)
+      const uint32_t ya[4] = {ta.x, ta.y, ta.z, ta.w}, yb[4] = {tb.x, tb.y, tb.z, tb.w};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+      for (int hw = 0; hw < 2; ++hw) {  // groups 4 hw .. 4 hw + 3
+        const uint32_t a_0 = hw ? va.y : va.x, a_1 = hw ? va.w : va.z;  // keys 2j, 2j + 1
+        const uint32_t b_0 = hw ? vb.y : vb.x, b_1 = hw ? vb.w : vb.z;  // keys 2j + 8, 2j + 9
+        uint32_t xl[4], xh[4], zl[4], zh[4];
+        constexpr uint32_t k = 0x0f0f0f0fu;
+        e2m1x8_f16((a_0 & k) | ((a_1 << 4) & ~k), xl);  // dim r of both keys
+        e2m1x8_f16(((a_0 >> 4) & k) | (a_1 & ~k), xh);  // dim r + 8
+        e2m1x8_f16((b_0 & k) | ((b_1 << 4) & ~k), zl);
+        e2m1x8_f16(((b_0 >> 4) & k) | (b_1 & ~k), zh);
+        uint32_t ga[4], gb[4];
+        e4m3x4_f16(ya[2 * hw], ga[0], ga[1]);
+        e4m3x4_f16(ya[2 * hw + 1], ga[2], ga[3]);
+        e4m3x4_f16(yb[2 * hw], gb[0], gb[1]);
+        e4m3x4_f16(yb[2 * hw + 1], gb[2], gb[3]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) mine[nt][i] = (row0 + 8 * nt + 2 * j + i) / a.G == t;
-        const uint32_t ya[4] = {ta.x & keep_a, ta.y & keep_a, ta.z & keep_a, ta.w & keep_a};
-        const uint32_t yb[4] = {tb.x & keep_b, tb.y & keep_b, tb.z & keep_b, tb.w & keep_b};
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t a0 = hmul2(xl[e], ga[e]), a1 = hmul2(xh[e], ga[e]);
+          const uint32_t a2 = hmul2(zl[e], gb[e]), a3 = hmul2(zh[e], gb[e]);
 #pragma unroll
-        for (int hw = 0; hw < 2; ++hw) {  // groups 4 hw .. 4 hw + 3
-          const uint32_t a_0 = hw ? va.y : va.x, a_1 = hw ? va.w : va.z;  // keys 2j, 2j + 1
-          const uint32_t b_0 = hw ? vb.y : vb.x, b_1 = hw ? vb.w : vb.z;  // keys 2j + 8, 2j + 9
-          uint32_t xl[4], xh[4], zl[4], zh[4];
-          constexpr uint32_t k = 0x0f0f0f0fu;
-          e2m1x8_f16((a_0 & k) | ((a_1 << 4) & ~k), xl);  // dim r of both keys
-          e2m1x8_f16(((a_0 >> 4) & k) | (a_1 & ~k), xh);  // dim r + 8
-          e2m1x8_f16((b_0 & k) | ((b_1 << 4) & ~k), zl);
-          e2m1x8_f16(((b_0 >> 4) & k) | (b_1 & ~k), zh);
-          uint32_t ga[4], gb[4];
-          e4m3x4_f16(ya[2 * hw], ga[0], ga[1]);
-          e4m3x4_f16(ya[2 * hw + 1], ga[2], ga[3]);
-          e4m3x4_f16(yb[2 * hw], gb[0], gb[1]);
-          e4m3x4_f16(yb[2 * hw + 1], gb[2], gb[3]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (part) {
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(d, a0, a1, a2, a3, p0[nt], p1[nt]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t a0 = hmul2(xl[e], ga[e]), a1 = hmul2(xh[e], ga[e]);
-            const uint32_t a2 = hmul2(zl[e], gb[e]), a3 = hmul2(zh[e], gb[e]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (part) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(d, a0, a1, a2, a3, p0[nt], p1[nt]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  if (mine[nt][q & 1]) o[4 * hw + e][nt][q] += d[q];
-              } else {
-                mma_f16(o[4 * hw + e][nt], a0, a1, a2, a3, p0[nt], p1[nt]);
-              }
+              for (int q = 0; q < 4; ++q)
+                if (mine[nt][q & 1]) o[4 * hw + e][nt][q] += d[q];
+            } else {
+              mma_f16(o[4 * hw + e][nt], a0, a1, a2, a3, p0[nt], p1[nt]);
             }
           }
         }
-      };
-      if (full) {
-        product(std::false_type{}, 0xffffffffu, 0xffffffffu, 0);
-      } else {
-        // once per query token, with the keys it sees
-        for (int t = t_lo; t <= t_hi; ++t) {
-          const int pt = rg.first_q + t;
-          auto keep = [&](int k0) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int key = tok0 + k0 + i;
-              if (valid && pt < rg.len && key <= pt && (a.window == 0 || key > pt - a.window || key < a.sinks))
-                m |= 0x00ff00ffu << (8 * i);
-            }
-            return m;
-          };
-          product(std::true_type{}, keep(2 * j), keep(2 * j + 8), t);
+      }
+    };
+
+    const int v_first = ua * kAttWarps + warp;
+    if (v_first < v_end) {
+      float c[NT][4];
+      cp_async_wait<kAttStages - 2>();
+      __syncwarp();  // every lane's copies have landed
+      scores(ring, c);
+      weights(c, v_first, (taken >> (kAttStages - 2)) & 1u);
+      uint32_t st = ring, nx = ring + kSubBytes;
+      for (int v = v_first; v < v_end; v += kAttWarps) {
+        cp_async_wait<kAttStages - 3>();
+        __syncwarp();  // the next stage is there, and the one before this is read out
+        issue();
+        const uint32_t scales = st + 2176 + 16 * j;
+        uint4 ta = lds128(scales), tb = lds128(scales + 64);
+        // (past the last sub-block: of whatever the stage holds, unused)
+        if (ONE || full) {
+          if (ONE && !full) {
+            const uint32_t ka = keep(2 * j, rg.first_q), kb = keep(2 * j + 8, rg.first_q);
+            ta = make_uint4(ta.x & ka, ta.y & ka, ta.z & ka, ta.w & ka);
+            tb = make_uint4(tb.x & kb, tb.y & kb, tb.z & kb, tb.w & kb);
+          }
+          scores(nx, c);
+          product(std::false_type{}, st, ta, tb, 0);
+        } else {
+          // once per query token, with the keys it sees
+          scores(nx, c);
+          for (int t = t_lo; t <= t_hi; ++t) {
+            const uint32_t ka = keep(2 * j, rg.first_q + t), kb = keep(2 * j + 8, rg.first_q + t);
+            product(std::true_type{}, st, make_uint4(ta.x & ka, ta.y & ka, ta.z & ka, ta.w & ka),
+                    make_uint4(tb.x & kb, tb.y & kb, tb.z & kb, tb.w & kb), t);
+          }
         }
+        if (v + kAttWarps < v_end) weights(c, v + kAttWarps, (taken >> (kAttStages - 2)) & 1u);
+        st = nx;
+        nx = nx == ring + (kAttStages - 1) * kSubBytes ? ring : nx + kSubBytes;
       }
     }
     cp_async_wait<0>();
@@ -499,6 +538,8 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
           ml[(warp * R + n) * 2 + 1] = l;
         }
       }
+    constexpr int kMergeStride = kAttStages * kSubBytes / 4;
+    float* merge = reinterpret_cast<float*>(smem + L::kRing);
     const bool whole = ua == 0 && ub == nu;
     const int slot = 2 * blockIdx.x + (first_part ? 0 : 1);
 #pragma unroll
@@ -508,19 +549,19 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
       for (int s = 0; s < 8; ++s)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          merge[(warp * 8 + 2 * j + (q & 1)) * 132 + 16 * s + r + 8 * (q >> 1)] = o[s][nt][q];
+          merge[warp * kMergeStride + (2 * j + (q & 1)) * 132 + 16 * s + r + 8 * (q >> 1)] = o[s][nt][q];
       __syncthreads();
       // warp w: row w of this group of eight, four dims a lane
       const int n = 8 * nt + warp, row = row0 + n;
-      float m = -INFINITY;
+      float m = kAttNoMax;
 #pragma unroll
       for (int w = 0; w < kAttWarps; ++w) m = fmaxf(m, ml[(w * R + n) * 2]);
       float l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kAttWarps; ++w) {
-        const float mw = ml[(w * R + n) * 2], f = mw == -INFINITY ? 0.f : ptx_exp2(mw - m);
-        const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + warp) * 132 + 4 * lane);
+        const float f = ptx_exp2(ml[(w * R + n) * 2] - m);
+        const float4 x = *reinterpret_cast<const float4*>(merge + w * kMergeStride + warp * 132 + 4 * lane);
         l = fmaf(f, ml[(w * R + n) * 2 + 1], l);
         acc.x = fmaf(f, x.x, acc.x);
         acc.y = fmaf(f, x.y, acc.y);
@@ -579,7 +620,7 @@ __global__ void __launch_bounds__(128) kv4_combine_kernel(const __grid_constant_
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows || parts == 1) return;  // one part: written by its CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float m = -INFINITY;
+  float m = kAttNoMax;
   for (int i = threadIdx.x; i < parts; i += 128) m = fmaxf(m, a.part_ml[at(i) * 2]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -589,7 +630,7 @@ __global__ void __launch_bounds__(128) kv4_combine_kernel(const __grid_constant_
   float l = 0.f;
   for (int i = threadIdx.x; i < parts; i += 128) {
     const float2 x = *reinterpret_cast<const float2*>(a.part_ml + at(i) * 2);
-    const float f = x.x == -INFINITY ? 0.f : ptx_exp2(x.x - m);
+    const float f = ptx_exp2(x.x - m);
     weight[i] = f;
     l = fmaf(f, x.y, l);
   }

@@ -106,12 +106,15 @@ rbs_status device_info(DeviceInfo** out) {
       e = e ? e : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(topk_smem_bytes(kTokMaxKV, kTokMaxKV / 32)));
     e = e ? e : cudaFuncSetAttribute(swa_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WinSmem::kAlloc);
-    e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     AttSmem<1>::bytes(kAttMaxBatch));
-    e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     AttSmem<2>::bytes(kAttMaxBatch));
-    e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     AttSmem<4>::bytes(kAttMaxBatch));
+#define RBS_KV4_ATTR(NT)                                                                                              \
+  e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,          \
+                                   AttSmem<NT>::bytes(kAttMaxBatch));                                                 \
+  e = e ? e : cudaFuncSetAttribute(kv4_attend_kernel<NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,         \
+                                   AttSmem<NT>::bytes(kAttMaxBatch));
+    RBS_KV4_ATTR(1)
+    RBS_KV4_ATTR(2)
+    RBS_KV4_ATTR(4)
+#undef RBS_KV4_ATTR
     e = e ? e : cudaFuncSetAttribute(block_beta_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RBS_MAX_KV_BLOCKS * 4);
     e = e ? e : cudaFuncSetAttribute(select_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RBS_MAX_KV_BLOCKS * 4);
     if (e != cudaSuccess) return fail(RBS_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -1420,7 +1423,8 @@ rbs_status kv4_attend(const rbs_bf16_tensor* Q, const rbs_kv4_cache* cache, cons
   const int64_t G = Q->heads / cache->kv_heads, rows = G * Q->seqlen;
   const int nt = attend_tiles_n(rows);
   const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
-  RBS_REQUIRE(static_cast<int64_t>(max_pages) * cache->page_size < (1ll << 31) &&
+  // lengths, and positions up to Lq past them, fit 32 bits
+  RBS_REQUIRE(static_cast<int64_t>(max_pages) * cache->page_size + Q->seqlen < (1ll << 31) &&
                   Q->batch * (static_cast<int64_t>(max_pages) * cache->page_size / (kAttWarps * kSubTokens) + 2) < (1ll << 31) &&
                   Q->batch * cache->kv_heads * tiles < (1ll << 31),
               RBS_ERR_UNSUPPORTED, "shape too large");
@@ -1436,6 +1440,7 @@ rbs_status kv4_attend(const rbs_bf16_tensor* Q, const rbs_kv4_cache* cache, cons
   a.G = static_cast<int>(G);
   a.page = cache->page_size;
   a.spp = cache->page_size / kSubTokens;
+  a.page_bytes = static_cast<uint32_t>(a.Hkv) * a.spp * kSubBytes;
   a.spp_magic = a.spp == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + a.spp - 1) / a.spp);
   a.table = block_table;
   a.table_b = table_stride;
@@ -1472,16 +1477,16 @@ rbs_status kv4_attend(const rbs_bf16_tensor* Q, const rbs_kv4_cache* cache, cons
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   cudaError_t e;
-  if (nt == 1) {
-    kv4_attend_kernel<1><<<a.ctas, kAttThreads, AttSmem<1>::bytes(a.B), stream>>>(a);
-    e = cudaLaunchKernelEx(&cfg, kv4_combine_kernel<1>, a);
-  } else if (nt == 2) {
-    kv4_attend_kernel<2><<<a.ctas, kAttThreads, AttSmem<2>::bytes(a.B), stream>>>(a);
-    e = cudaLaunchKernelEx(&cfg, kv4_combine_kernel<2>, a);
-  } else {
-    kv4_attend_kernel<4><<<a.ctas, kAttThreads, AttSmem<4>::bytes(a.B), stream>>>(a);
-    e = cudaLaunchKernelEx(&cfg, kv4_combine_kernel<4>, a);
-  }
+#define RBS_KV4_LAUNCH(NT)                                                                                       \
+  do {                                                                                                           \
+    if (a.Lq == 1) kv4_attend_kernel<NT, true><<<a.ctas, kAttThreads, AttSmem<NT>::bytes(a.B), stream>>>(a);     \
+    else kv4_attend_kernel<NT, false><<<a.ctas, kAttThreads, AttSmem<NT>::bytes(a.B), stream>>>(a);              \
+    e = cudaLaunchKernelEx(&cfg, kv4_combine_kernel<NT>, a);                                                     \
+  } while (0)
+  if (nt == 1) RBS_KV4_LAUNCH(1);
+  else if (nt == 2) RBS_KV4_LAUNCH(2);
+  else RBS_KV4_LAUNCH(4);
+#undef RBS_KV4_LAUNCH
   if ((st = check_launch("kv4_attend_kernel")) != RBS_OK) return st;
   if (e != cudaSuccess) return fail(RBS_ERR_CUDA, "kv4_combine_kernel: %s", cudaGetErrorString(e));
   return RBS_OK;
