@@ -202,20 +202,52 @@ __device__ __forceinline__ uint32_t quantise16(const uint4& x0, const uint4& x1,
     finite = finite && (w[i] & 0x7f80u) != 0x7f80u && (w[i] & 0x7f800000u) != 0x7f800000u;
     amax = fmax3(amax, fabsf(x[2 * i]), fabsf(x[2 * i + 1]));
   }
+  // amax / 6 on a border between two scales is exact (the border has 5
+  // significant bits and amax 8), so ties go to the even scale
   const uint32_t s8 = finite ? e4m3_bits(__fdiv_rn(amax, 6.f)) : 0x7fu;
   const float s = e4m3_value(s8);
   const bool zero = !finite || s8 == 0;
+  // x / s as x times 1 / s, off by at most 2^-22 relative, then brought to
+  // multiples of 2^-11: x has 8 significant bits and a border between two codes
+  // (1, 3, 5, 7 quarters or halves, 5) times s at most 7, so a quotient that is
+  // not on a border is 2^-8 of it, 2^-10 at least, away from it and stays on
+  // its side, and one that is on a border becomes it: ties go to the even code
+  const float inv = zero ? 0.f : __frcp_rn(s);
+  const float2 inv2 = make_float2(inv, inv), up = make_float2(0x1p12f, 0x1p12f), down = make_float2(-0x1p12f, -0x1p12f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float lo = KEY ? x[2 * i] : x[i], hi = KEY ? x[2 * i + 1] : x[i + 8];
-    // IEEE division: a quotient that lies on a border between two codes is
-    // exact (x has 8 significant bits and s 4), so ties go to the even code
-    q[i] = zero ? 0u : e2m1x2(__fdiv_rn(lo, s), __fdiv_rn(hi, s));
+    float2 y = make_float2(KEY ? x[2 * i] : x[i], KEY ? x[2 * i + 1] : x[i + 8]);
+    const uint32_t sign = (__float_as_uint(y.x) >> 28 & 8u) | (__float_as_uint(y.y) >> 24 & 0x80u);
+    y = fadd2(fadd2(fmul2(y, inv2), up), down);
+    // (the sum loses the sign of what becomes zero)
+    q[i] = zero ? 0u : e2m1x2(y.x, y.y) | sign;
   }
   return s8;
 }
 
-// One thread per (token, head, group), eight neighbours to a token's row.
+// Eight neighbouring lanes with eight bytes each, lo and hi: lane i's byte k
+// becomes lane k's byte i, by one exchange for each of the lane's three bits.
+__device__ __forceinline__ void transpose8(uint32_t& lo, uint32_t& hi, int lane, uint32_t group) {
+  const bool b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
+  uint32_t got = __shfl_xor_sync(group, b2 ? lo : hi, 4);
+  if (b2) lo = got; else hi = got;
+  // pairs of bytes: the lane whose bit is clear keeps bytes 0, 1 of both words
+  uint32_t mine = __byte_perm(lo, hi, b1 ? 0x7632 : 0x5410);
+  got = __shfl_xor_sync(group, __byte_perm(lo, hi, b1 ? 0x5410 : 0x7632), 2);
+  lo = __byte_perm(b1 ? got : mine, b1 ? mine : got, 0x5410);
+  hi = __byte_perm(b1 ? got : mine, b1 ? mine : got, 0x7632);
+  // single bytes: bytes 0 and 2 of both
+  mine = __byte_perm(lo, hi, b0 ? 0x7531 : 0x6420);
+  got = __shfl_xor_sync(group, __byte_perm(lo, hi, b0 ? 0x6420 : 0x7531), 1);
+  lo = __byte_perm(b0 ? got : mine, b0 ? mine : got, 0x5140);
+  hi = __byte_perm(b0 ? got : mine, b0 ? mine : got, 0x7362);
+}
+
+// One thread per (token, head, group of dims), eight neighbours to a token's
+// row, which move their bytes to the layout's order among themselves: a thread
+// writes (reads) eight bytes of the row's key codes and eight of its value
+// codes.  Bound by memory, 512 + 144 bytes per row, and for less than some
+// thousand tokens by the launch.
 __global__ void __launch_bounds__(kIoThreads) kv4_append_kernel(const __grid_constant__ Kv4IoArgs a) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kIoThreads / 8) + (threadIdx.x >> 3);
   const int s = threadIdx.x & 7;
@@ -235,14 +267,26 @@ __global__ void __launch_bounds__(kIoThreads) kv4_append_kernel(const __grid_con
   int t;
   uint8_t* sub = kv4_sub(a.data, a.Hkv, a.page, slot, h, t);
   const int hh = t >> 3, r = t & 7, j = r >> 1, i = r & 1;
+  const uint32_t group = 0xffu << (threadIdx.x & 24);
+  auto word = [](const uint32_t* q) { return q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24; };
   uint32_t q[8];
   sub[2048 + 8 * t + s] = static_cast<uint8_t>(quantise16<true>(k0, k1, a.kg_inv, q));
-#pragma unroll
-  for (int jj = 0; jj < 4; ++jj)
-    *reinterpret_cast<uint16_t*>(sub + 512 * hh + 64 * r + 16 * jj + 2 * s) = static_cast<uint16_t>(q[jj] | (q[4 + jj] << 8));
+  {
+    // byte 2 j + e from every group: lane 2 j + e then has byte e of chunk j of all of them
+    const uint32_t m[8] = {q[0], q[4], q[1], q[5], q[2], q[6], q[3], q[7]};
+    uint32_t lo = word(m), hi = word(m + 4);
+    transpose8(lo, hi, s, group);
+    // bytes of e = 0 and e = 1 alternate: the even lane takes groups 0 .. 3, the odd one 4 .. 7
+    const uint32_t got = __shfl_xor_sync(group, s & 1 ? lo : hi, 1);
+    const uint32_t x = s & 1 ? got : lo, y = s & 1 ? hi : got;
+    *reinterpret_cast<uint2*>(sub + 512 * hh + 64 * r + 8 * s) = make_uint2(__byte_perm(x, y, 0x5140), __byte_perm(x, y, 0x7362));
+  }
   sub[2176 + 16 * (t >> 1) + 2 * s + i] = static_cast<uint8_t>(quantise16<false>(v0, v1, a.vg_inv, q));
-#pragma unroll
-  for (int rr = 0; rr < 8; ++rr) sub[1024 + 512 * hh + 64 * rr + 16 * j + 8 * i + s] = static_cast<uint8_t>(q[rr]);
+  {
+    uint32_t lo = word(q), hi = word(q + 4);
+    transpose8(lo, hi, s, group);  // lane r: dims r and r + 8 of every group
+    *reinterpret_cast<uint2*>(sub + 1024 + 512 * hh + 64 * s + 16 * j + 8 * i) = make_uint2(lo, hi);
+  }
 }
 
 __global__ void __launch_bounds__(kIoThreads) kv4_load_kernel(const __grid_constant__ Kv4IoArgs a) {
@@ -262,23 +306,32 @@ __global__ void __launch_bounds__(kIoThreads) kv4_load_kernel(const __grid_const
     const uint8_t* sub = kv4_sub(a.data, a.Hkv, a.page, slot, h, t);
     const int hh = t >> 3, r = t & 7, j = r >> 1, i = r & 1;
     const float ks = e4m3_value(sub[2048 + 8 * t + s]) * a.kg, vs = e4m3_value(sub[2176 + 16 * (t >> 1) + 2 * s + i]) * a.vg;
+    const uint32_t group = 0xffu << (threadIdx.x & 24);
+    {
+      const uint2 w = *reinterpret_cast<const uint2*>(sub + 512 * hh + 64 * r + 8 * s);
+      const uint32_t x = __byte_perm(w.x, w.y, 0x6420), y = __byte_perm(w.x, w.y, 0x7531);
+      const uint32_t got = __shfl_xor_sync(group, s & 1 ? x : y, 1);
+      uint32_t lo = s & 1 ? got : x, hi = s & 1 ? y : got;
+      transpose8(lo, hi, s, group);  // byte 2 j + e of this group
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj) {
-      const uint32_t two = *reinterpret_cast<const uint16_t*>(sub + 512 * hh + 64 * r + 16 * jj + 2 * s);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t f = e2m1x2_f16((two >> (8 * e)) & 0xffu);
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t f = e2m1x2_f16(((k < 4 ? lo : hi) >> (8 * (k & 3))) & 0xffu);
         const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-        ko[4 * e + jj] = pack_bf16x2(v.x * ks, v.y * ks);
+        ko[4 * (k & 1) + (k >> 1)] = pack_bf16x2(v.x * ks, v.y * ks);
       }
     }
     float lo[8], hi[8];
+    {
+      const uint2 w = *reinterpret_cast<const uint2*>(sub + 1024 + 512 * hh + 64 * s + 16 * j + 8 * i);
+      uint32_t x = w.x, y = w.y;
+      transpose8(x, y, s, group);  // byte r of this group
 #pragma unroll
-    for (int rr = 0; rr < 8; ++rr) {
-      const uint32_t f = e2m1x2_f16(sub[1024 + 512 * hh + 64 * rr + 16 * j + 8 * i + s]);
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-      lo[rr] = v.x * vs;
-      hi[rr] = v.y * vs;
+      for (int rr = 0; rr < 8; ++rr) {
+        const uint32_t f = e2m1x2_f16(((rr < 4 ? x : y) >> (8 * (rr & 3))) & 0xffu);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+        lo[rr] = v.x * vs;
+        hi[rr] = v.y * vs;
+      }
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
