@@ -497,9 +497,9 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
         issue();
         const uint32_t scales = st + 2176 + 16 * j;
         uint4 ta = lds128(scales), tb = lds128(scales + 64);
-        // (past the last sub-block: of whatever the stage holds, unused)
-        if (ONE || full) {
-          if (ONE && !full) {
+        // (scores past the last sub-block: of whatever the stage holds, unused)
+        if (ONE) {
+          if (!full) {
             const uint32_t ka = keep(2 * j, rg.first_q), kb = keep(2 * j + 8, rg.first_q);
             ta = make_uint4(ta.x & ka, ta.y & ka, ta.z & ka, ta.w & ka);
             tb = make_uint4(tb.x & kb, tb.y & kb, tb.z & kb, tb.w & kb);
@@ -507,12 +507,16 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
           scores(nx, c);
           product(std::false_type{}, st, ta, tb, 0);
         } else {
-          // once per query token, with the keys it sees
           scores(nx, c);
-          for (int t = t_lo; t <= t_hi; ++t) {
-            const uint32_t ka = keep(2 * j, rg.first_q + t), kb = keep(2 * j + 8, rg.first_q + t);
-            product(std::true_type{}, st, make_uint4(ta.x & ka, ta.y & ka, ta.z & ka, ta.w & ka),
-                    make_uint4(tb.x & kb, tb.y & kb, tb.z & kb, tb.w & kb), t);
+          if (full) {
+            product(std::false_type{}, st, ta, tb, 0);
+          } else {
+            // once per query token, with the keys it sees
+            for (int t = t_lo; t <= t_hi; ++t) {
+              const uint32_t ka = keep(2 * j, rg.first_q + t), kb = keep(2 * j + 8, rg.first_q + t);
+              product(std::true_type{}, st, make_uint4(ta.x & ka, ta.y & ka, ta.z & ka, ta.w & ka),
+                      make_uint4(tb.x & kb, tb.y & kb, tb.z & kb, tb.w & kb), t);
+            }
           }
         }
         if (v + kAttWarps < v_end) weights(c, v + kAttWarps, (taken >> (kAttStages - 2)) & 1u);

@@ -48,7 +48,7 @@ constexpr int kQkThreads = 128;
 constexpr int kQkHeads = 4;  // head rows whose loads are in flight together
 
 template <int STYLE>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const __grid_constant__ QkNormArgs a) {
+__global__ void __launch_bounds__(kQkThreads, 5) qk_norm_rope_kernel(const __grid_constant__ QkNormArgs a) {
   const int c = threadIdx.x & 7;
   const int64_t u = static_cast<int64_t>(blockIdx.x) * (kQkThreads / 8) + (threadIdx.x >> 3);
   if (u >= a.units) return;  // the eight threads of a unit stay together
