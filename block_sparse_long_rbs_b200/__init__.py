@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import math
 
 import torch
@@ -398,13 +399,16 @@ def _table(x, name: str, dev: torch.device, rows: int) -> tuple[int, int, int]:
     """Pointer, row stride and width of an int32 [rows, width] table with contiguous rows on dev."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if x.dtype != torch.int32 or x.dim() != 2 or x.stride(1) != 1:
+    if x.dtype is not torch.int32 or x.dim() != 2:
         raise TypeError(f"{name}: expected an int32 CUDA tensor [batch, max_pages] with contiguous rows")
-    if x.shape[0] != rows:
-        raise ValueError(f"{name}: expected {rows} rows, got {x.shape[0]}")
+    (n, width), (stride, inner) = x.shape, x.stride()
+    if inner != 1 and width > 1:
+        raise TypeError(f"{name}: expected an int32 CUDA tensor [batch, max_pages] with contiguous rows")
+    if n != rows:
+        raise ValueError(f"{name}: expected {rows} rows, got {n}")
     if x.device != dev:
         raise ValueError(f"{name} is on {x.device}, expected {dev}: every tensor of a call must be on one device")
-    return x.data_ptr(), max(x.stride(0), x.shape[1]) if rows == 1 else x.stride(0), x.shape[1]
+    return x.data_ptr(), stride if rows > 1 else max(stride, width), width
 
 
 def rope_qk_norm(Q: torch.Tensor, K: torch.Tensor, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
@@ -483,12 +487,13 @@ class KV4Cache:
         x = self.data
         if not isinstance(x, torch.Tensor):
             raise TypeError("cache.data: expected a torch.Tensor")
-        if not x.is_cuda or x.dtype != torch.uint8 or not x.is_contiguous() or x.dim() != 3:
+        if not x.is_cuda or x.dtype is not torch.uint8 or not x.is_contiguous() or x.dim() != 3:
             raise TypeError("cache.data: expected a contiguous uint8 CUDA tensor [num_pages, Hkv, page bytes]")
+        pages, heads, size = x.shape
         # a page is page_size / 16 sub-blocks of 2304 bytes; the library checks the page size itself
-        if x.shape[2] != self.page_size // 16 * 2304:
-            raise ValueError(f"cache.data: pages of {x.shape[2]} bytes, expected {self.page_size // 16 * 2304}")
-        return KV4CacheC(x.data_ptr(), x.shape[0], x.shape[1], self.page_size, self.k_scale, self.v_scale)
+        if size != self.page_size // 16 * 2304:
+            raise ValueError(f"cache.data: pages of {size} bytes, expected {self.page_size // 16 * 2304}")
+        return KV4CacheC(x.data_ptr(), pages, heads, self.page_size, self.k_scale, self.v_scale)
 
 
 def kv4_extend(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
@@ -546,6 +551,7 @@ def kv4_load(cache: KV4Cache, slots: torch.Tensor, k_out: torch.Tensor | None = 
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=256)  # a function of the sizes alone
 def rbs_kv4_attend_workspace_bytes(seqlen_q: int, heads_q: int, kv_heads: int) -> int:
     return int(lib().rbs_kv4_attend_workspace_bytes(seqlen_q, heads_q, kv_heads))
 
