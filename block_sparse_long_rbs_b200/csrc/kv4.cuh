@@ -191,17 +191,16 @@ __device__ __forceinline__ float e4m3_value(uint32_t bits) {
 template <bool KEY>
 __device__ __forceinline__ uint32_t quantise16(const uint4& x0, const uint4& x1, float g_inv, uint32_t (&q)[8]) {
   const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-  float x[16], amax = 0.f;
-  bool finite = true;
+  // the largest size by its bits, two values at a time: infinities and NaN are
+  // above every finite one
+  uint32_t top = w[0] & 0x7fff7fffu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // g is a power of two: an exact shift (a result below fp32's normal
-    // range is below any code)
-    x[2 * i] = bf16lo(w[i]) * g_inv;
-    x[2 * i + 1] = bf16hi(w[i]) * g_inv;
-    finite = finite && (w[i] & 0x7f80u) != 0x7f80u && (w[i] & 0x7f800000u) != 0x7f800000u;
-    amax = fmax3(amax, fabsf(x[2 * i]), fabsf(x[2 * i + 1]));
-  }
+  for (int i = 1; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+  top = max(top & 0xffffu, top >> 16);
+  const bool finite = top < 0x7f80u;
+  // g is a power of two: an exact shift (a result below fp32's normal range is
+  // below any code)
+  const float amax = __uint_as_float(top << 16) * g_inv;
   // amax / 6 on a border between two scales is exact (the border has 5
   // significant bits and amax 8), so ties go to the even scale
   const uint32_t s8 = finite ? e4m3_bits(__fdiv_rn(amax, 6.f)) : 0x7fu;
@@ -212,13 +211,17 @@ __device__ __forceinline__ uint32_t quantise16(const uint4& x0, const uint4& x1,
   // (1, 3, 5, 7 quarters or halves, 5) times s at most 7, so a quotient that is
   // not on a border is 2^-8 of it, 2^-10 at least, away from it and stays on
   // its side, and one that is on a border becomes it: ties go to the even code
+  // (a value above s's range is infinite here at most, and 6 below)
   const float inv = zero ? 0.f : __frcp_rn(s);
-  const float2 inv2 = make_float2(inv, inv), up = make_float2(0x1p12f, 0x1p12f), down = make_float2(-0x1p12f, -0x1p12f);
+  const float2 g2 = make_float2(g_inv, g_inv), inv2 = make_float2(inv, inv);
+  const float2 up = make_float2(0x1p12f, 0x1p12f), down = make_float2(-0x1p12f, -0x1p12f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float2 y = make_float2(KEY ? x[2 * i] : x[i], KEY ? x[2 * i + 1] : x[i + 8]);
+    const int j = i >> 1;  // values: words j and 4 + j, halves i % 2
+    float2 y = KEY ? make_float2(bf16lo(w[i]), bf16hi(w[i]))
+                   : make_float2(i & 1 ? bf16hi(w[j]) : bf16lo(w[j]), i & 1 ? bf16hi(w[4 + j]) : bf16lo(w[4 + j]));
     const uint32_t sign = (__float_as_uint(y.x) >> 28 & 8u) | (__float_as_uint(y.y) >> 24 & 0x80u);
-    y = fadd2(fadd2(fmul2(y, inv2), up), down);
+    y = fadd2(fadd2(fmul2(fmul2(y, g2), inv2), up), down);
     // (the sum loses the sign of what becomes zero)
     q[i] = zero ? 0u : e2m1x2(y.x, y.y) | sign;
   }
