@@ -363,3 +363,52 @@ def test_attend_layouts_streams_graph(cuda_ok):
         g.replay()
         a, b = rbs.kv4_attend(Q, held.cache, table, lens, return_lse=True)
         assert torch.equal(o, a) and torch.equal(z, b)
+
+
+@pytest.mark.parametrize("B", [1500, 4096])
+def test_attend_many_requests(cuda_ok, B):
+    """Up to the most requests of a call, of a few tokens each, some of none."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 40, B)
+    held = Held(rng, lens, 1, 16)
+    Q = randn(rng, B, 1, 2, 128)
+    o, lse = _attend(held, Q)
+    pick = np.r_[0:20, rng.integers(0, B, 100), B - 20:B]
+    part = Held.__new__(Held)
+    part.lens, part.k, part.v = held.lens[pick], held.k[pick], held.v[pick]
+    _check(o[pick], lse[pick], part, Q[pick])
+    assert (f64(lse)[lens == 0] == -np.inf).all() and not f64(o)[lens == 0].any()
+
+
+def test_cache_past_32_bits(cuda_ok):
+    """Pages whose bytes lie beyond 2^31 and 2^32 of a cache of 4.7 GB."""
+    rng = np.random.default_rng(60)
+    page, H, pages = 256, 8, 16000
+    data = torch.empty(pages, H, rbs.rbs_kv4_page_bytes(page), dtype=torch.uint8, device="cuda")
+    assert data.numel() > 1 << 32
+    cache = rbs.KV4Cache(data, page)
+    table = np.array([[pages - 1, 7, 15000], [7300, 14600, 0]])
+    lens = np.array([600, 300])
+    K, V = randn(rng, 2, 600, H, 128), randn(rng, 2, 600, H, 128)
+    t = np.arange(600)
+    slots = np.where(t < lens[:, None], table[np.arange(2)[:, None], t // page] * page + t % page, -1)
+    rbs.kv4_append(cache, K, V, ints(slots))
+    k, v = rbs.kv4_load(cache, ints(slots))
+    held = Held.__new__(Held)
+    held.lens, held.k, held.v = lens, S.round_trip(f64(K)), S.round_trip(f64(V))
+    for b in range(2):
+        assert np.array_equal(f64(k)[b, :lens[b]], held.k[b, :lens[b]])
+        assert np.array_equal(f64(v)[b, :lens[b]], held.v[b, :lens[b]])
+    Q = randn(rng, 2, 1, 16, 128)
+    o, lse = rbs.kv4_attend(Q, cache, ints(table), ints(lens), return_lse=True)
+    _check(o, lse, held, Q)
+
+
+def test_attend_a_prompt(cuda_ok):
+    """Many query tokens per request: tiles of rows that end inside a token's heads, and several of them per request."""
+    rng = np.random.default_rng(61)
+    held = Held(rng, [150, 64], 2, 32)
+    Q = randn(rng, 2, 64, 6, 128)
+    for kw in ({}, dict(window=20, sinks=2)):
+        o, lse = _attend(held, Q, **kw)
+        _check(o, lse, held, Q, **kw)

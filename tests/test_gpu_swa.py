@@ -134,3 +134,19 @@ def test_nan_and_infinity_in_masked_places(cuda_ok, G):
         assert np.array_equal(~np.isfinite(got), odd)
         assert (np.abs(got - f64(want)[0, :, h])[~odd] <= off[0, :, h][~odd]).all()
         assert np.array_equal(f64(lse)[0, h, ~bad_k], f64(wlse)[0, h, ~bad_k])
+
+
+def test_batches_far_apart(cuda_ok):
+    """Batch entries more than 2^31 bytes apart (views of one buffer)."""
+    rng = np.random.default_rng(35)
+    big = torch.empty(2, (1 << 30) + 4096, dtype=torch.bfloat16, device="cuda")
+    x = randn(rng, 2, 100, 12, 128)
+    qkv = big[:, :x[0].numel()].view(2, 100, 12, 128)
+    qkv.copy_(x)
+    out = big[:, 1 << 20:(1 << 20) + 100 * 8 * 128].view(2, 100, 8, 128)
+    _check(qkv[:, :, :8], qkv[:, :, 8:10], qkv[:, :, 10:], 30, 3, out=out)
+    w = randn(rng, 128)
+    pos = torch.arange(100, dtype=torch.int32, device="cuda")
+    got = rbs.rope_qk_norm(qkv[:, :, :8], qkv[:, :, 8:10], w, None, pos, 1e4, q_out=out)
+    want = rbs.rope_qk_norm(x[:, :, :8], x[:, :, 8:10], w, None, pos, 1e4)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
