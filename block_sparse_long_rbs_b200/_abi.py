@@ -89,6 +89,8 @@ SIGNATURES = {
                                   P(Bf16Tensor), vp, vp]),
     "rbs_testing_bsa_prefill_stalled": (ctypes.c_int, [P(Bf16Tensor), P(Bf16Tensor), P(Bf16Tensor), P(BlockListsC),
                                                        i32, i32, ctypes.c_uint64, i32, P(Bf16Tensor), vp]),
+    "rbs_testing_swa_prefill_stalled": (ctypes.c_int, [P(Bf16Tensor), P(Bf16Tensor), P(Bf16Tensor), i32,
+                                                       ctypes.c_uint64, i32, P(Bf16Tensor), vp]),
     "rbs_testing_exp2": (ctypes.c_int, [vp, vp, i64, vp]),
 }
 

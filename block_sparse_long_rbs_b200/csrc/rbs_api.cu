@@ -1193,13 +1193,10 @@ rbs_status make_group_map(const rbs_bf16_tensor* t, int heads, int rows, CUtenso
   return RBS_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-rbs_status swa_prefill(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const rbs_bf16_tensor* V, int32_t window,
-                       int32_t sinks, int64_t q_offset, float softmax_scale, rbs_bf16_tensor* O, float* lse,
-                       rbs_stream_t stream) {
+// wait_ns, stall_after: for the library's own tests, as in BsaExtra.
+rbs_status launch_swa(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const rbs_bf16_tensor* V, int32_t window,
+                      int32_t sinks, int64_t q_offset, float softmax_scale, rbs_bf16_tensor* O, float* lse,
+                      rbs_stream_t stream, uint64_t wait_ns = kWaitLimitNs, int stall_after = -1) {
   rbs_status st;
   if ((st = check_tensor(Q, "Q")) != RBS_OK) return st;
   if ((st = check_tensor(K, "K")) != RBS_OK) return st;
@@ -1258,10 +1255,30 @@ rbs_status swa_prefill(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const
   a.inv_hkv = 1.f / static_cast<float>(a.Hkv);
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(RBS_HEAD_DIM));
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.wait_ns = kWaitLimitNs;
+  a.wait_ns = wait_ns;
+  a.stall_after = stall_after;
   const int grid = static_cast<int>(std::min<int64_t>(items, 2 * di->sms));
   swa_prefill_kernel<<<grid, kWinThreads, WinSmem::kAlloc, stream>>>(a);
   return check_launch("swa_prefill_kernel");
+}
+
+}  // namespace
+
+extern "C" {
+
+rbs_status swa_prefill(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const rbs_bf16_tensor* V, int32_t window,
+                       int32_t sinks, int64_t q_offset, float softmax_scale, rbs_bf16_tensor* O, float* lse,
+                       rbs_stream_t stream) {
+  return launch_swa(Q, K, V, window, sinks, q_offset, softmax_scale, O, lse, stream);
+}
+
+rbs_status rbs_testing_swa_prefill_stalled(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K,
+                                           const rbs_bf16_tensor* V, int32_t window, uint64_t wait_ns,
+                                           int32_t stall_after, rbs_bf16_tensor* O, rbs_stream_t stream) {
+  RBS_REQUIRE(wait_ns >= 100000ull && wait_ns <= kWaitLimitNs, RBS_ERR_INVALID_ARG,
+              "wait_ns must be in [1e5, %llu]", static_cast<unsigned long long>(kWaitLimitNs));
+  RBS_REQUIRE(stall_after >= 0, RBS_ERR_INVALID_ARG, "stall_after must be >= 0");
+  return launch_swa(Q, K, V, window, 0, 0, 0.f, O, nullptr, stream, wait_ns, stall_after);
 }
 
 }  // extern "C"

@@ -62,6 +62,7 @@ struct WinArgs {
   float inv_nt, inv_hkv;
   float scale_log2;
   uint64_t wait_ns;
+  int stall_after;  // testing only: the K producer stops after this many tiles (< 0: never)
 };
 
 constexpr int kWinThreads = 256;
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
           ++nq;
         }
         for (int t = 0; t < x.n; ++t) {
+          if (isK && a.stall_after >= 0 && static_cast<int>(nf) >= a.stall_after) { ok = false; break; }
           const int s = nf % kWinNS;
           // the stage's previous tile is consumed: its S (for K) or PV (for V)
           // is complete.  Neither barrier can move past that phase before this

@@ -525,6 +525,11 @@ RBS_API rbs_status rbs_testing_bsa_prefill_stalled(const rbs_bf16_tensor* Q, con
                                                    const rbs_bf16_tensor* V, const rbs_block_lists* lists,
                                                    int32_t block_q, int32_t block_k, uint64_t wait_ns,
                                                    int32_t stall_after, rbs_bf16_tensor* O, rbs_stream_t stream);
+/* rbs_testing_swa_prefill_stalled: swa_prefill (no sinks, no LSE, default
+ *   scale) stalled the same way, stall_after counting each block's key tiles. */
+RBS_API rbs_status rbs_testing_swa_prefill_stalled(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K,
+                                                   const rbs_bf16_tensor* V, int32_t window, uint64_t wait_ns,
+                                                   int32_t stall_after, rbs_bf16_tensor* O, rbs_stream_t stream);
 RBS_API rbs_status rbs_testing_exp2(const float* x, float* y, int64_t n, rbs_stream_t stream);
 
 #ifdef __cplusplus

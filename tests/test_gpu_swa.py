@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import block_sparse_long_rbs_b200 as rbs
+from block_sparse_long_rbs_b200 import _abi, _stream, _t
 from oracle import serving_oracle as S
 from serving_helpers import BF16, check_attention, f64, randn
 
@@ -150,3 +151,21 @@ def test_batches_far_apart(cuda_ok):
     got = rbs.rope_qk_norm(qkv[:, :, :8], qkv[:, :, 8:10], w, None, pos, 1e4, q_out=out)
     want = rbs.rope_qk_norm(x[:, :, :8], x[:, :, 8:10], w, None, pos, 1e4)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("stall", [0, 1, 5])
+def test_wait_that_runs_out_returns_timeout_and_the_next_call_is_correct(cuda_ok, stall):
+    """The producer of key tiles stops early (a testing hook): the waits for the missing tiles run out, the kernel records
+    it and returns with nothing in flight, and the next call is correct."""
+    rng = np.random.default_rng(36)
+    Q, K, V = _qkv(rng, 1, 3000, 8, 2)
+    out = torch.zeros_like(Q)
+    L_ = _abi.lib()
+    assert rbs.rbs_get_device_error() == 0
+    args = (_t(Q, "Q"), _t(K, "K"), _t(V, "V"), 500)
+    assert L_.rbs_testing_swa_prefill_stalled(*args, 1_000_000, stall, _t(out, "O"), _stream()) == 0, L_.rbs_last_error()
+    torch.cuda.synchronize()
+    assert rbs.rbs_get_device_error() & rbs.DEVERR_TIMEOUT
+    _check(Q, K, V, 500, 4, rows=np.unique(rng.integers(0, 3000, 40)))
+    for wait, n in ((10, 5), (3_000_000_000, 5), (1_000_000, -1)):
+        assert L_.rbs_testing_swa_prefill_stalled(*args, wait, n, _t(out, "O"), _stream()) == 1
