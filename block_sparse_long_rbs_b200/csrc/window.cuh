@@ -31,10 +31,12 @@
 // overlap them with only part of their other work (1890 cycles per pair of
 // tiles measured; the products need 1280: 48 cycles per K = 16 step of S at
 // N = 64, where shared memory is the limit, and 64 of P V).  Measured and left,
-// 16,384 tokens, window 4096, 32 q / 4 KV heads, 892 us as here: one CTA with two
-// row tiles on shared key tiles (1056 us: the two run in step, and their
-// exponentials collide), key tiles of 128 in that form (1120 us), a quarter of
-// the exponentials as a polynomial (915 us).
+// 16,384 tokens, window 4096, 32 q / 4 KV heads, 892 us as here (1030 us when
+// repeated until the power limit lowers the clock): one CTA with two row tiles on
+// shared key tiles (1056 us: the two run in step, and their exponentials
+// collide), key tiles of 128 in that form (1120 us), a quarter of the
+// exponentials as a polynomial (915 us), two warps per row with the maximum
+// agreed between them (1005 us).
 //
 // Masked scores are replaced before the softmax, so NaN keys stay out; a NaN or
 // infinite value in a masked place still meets a zero weight in the product.
