@@ -31,6 +31,7 @@ from ._abi import (  # noqa: F401
     RbsError,
     SelectParamsC,
     check,
+    fast,
     lib,
 )
 
@@ -351,9 +352,18 @@ def rope_reencode(x: torch.Tensor, old_pos: torch.Tensor, new_pos: torch.Tensor,
 
 
 # ---- serving: norm and rotation, the 4-bit cache ----------------------------
-# These run once per layer and decoding step, where the call itself counts:
-# the current device is switched only when it is another one, and the stream
-# is taken as a raw handle.
+# These run once per layer and decoding step, where the call itself counts.
+# Each first hands its arguments to the native marshalling (csrc/fastcall.cpp),
+# which makes the call when they are plainly what it takes, on the current
+# device; otherwise the code here checks them one by one, says what is wrong,
+# and makes the call on another device.
+
+
+def _made(result, where: str):
+    """What the native marshalling returned: the outputs, or a status that is an error."""
+    if type(result) is int:
+        check(result, where)
+    return result
 
 
 def _b(x, name: str) -> Bf16Tensor:
@@ -416,6 +426,9 @@ def rope_qk_norm(Q: torch.Tensor, K: torch.Tensor, q_weight: torch.Tensor | None
                  q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
     """Per-head norm of queries and keys and their rotation to pos ([L] or [B, L] int32), one pass.
     Returns (q_out, k_out); an output may be its input, for in place."""
+    made = fast().rope_qk_norm(Q, K, q_weight, k_weight, pos, theta, eps, rope_style, q_out, k_out)
+    if made is not None:
+        return _made(made, "rope_qk_norm")
     if q_out is None:
         q_out = torch.empty_like(Q)
     if k_out is None:
@@ -446,6 +459,9 @@ def swa_prefill(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, window: int, 
                 softmax_scale: float | None = None, out: torch.Tensor | None = None, return_lse: bool = False):
     """Causal attention of Q [B, Lq, Hq, 128] over K, V [B, Lk, Hkv, 128] where the query at position p = t + q_offset
     sees the last `window` keys up to its own and the first `sinks` (window 0: every key up to its own)."""
+    made = fast().swa_prefill(Q, K, V, window, sinks, q_offset, softmax_scale, out, return_lse)
+    if made is not None:
+        return _made(made, "swa_prefill")
     tq, tk, tv = _b(Q, "Q"), _b(K, "K"), _b(V, "V")
     dev = Q.device
     if out is None:
@@ -502,6 +518,10 @@ def kv4_extend(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torc
     """Pages from the free list for requests that grow from old_lens to new_lens ([B] int32): updates block_table
     [B, max_pages] in place and returns (slots, pos, free_head_out), the slots and positions [B, max_new] of the new
     tokens (-1 past a request's last one) and the count of free pages taken so far."""
+    made = fast().kv4_extend(block_table, old_lens, new_lens, free_pages, free_head, max_new, page_size, slots, pos,
+                             free_head_out)
+    if made is not None:
+        return _made(made, "kv4_extend")
     if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
         raise TypeError("block_table: expected a CUDA tensor")
     dev, B = block_table.device, block_table.shape[0]
@@ -526,6 +546,10 @@ def kv4_extend(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torc
 
 def kv4_append(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor) -> None:
     """Quantise K and V [B, L, Hkv, 128] into the cache's slots [B, L] (int32; negative: padding, skipped)."""
+    made = fast().kv4_append(cache.data, cache.page_size, cache.k_scale, cache.v_scale, K, V, slots)
+    if made is not None:
+        _made(made, "kv4_append")
+        return
     tk, tv, c = _b(K, "K"), _b(V, "V"), cache.c()
     dev = K.device
     if V.device != dev or cache.data.device != dev:
@@ -536,6 +560,9 @@ def kv4_append(cache: KV4Cache, K: torch.Tensor, V: torch.Tensor, slots: torch.T
 def kv4_load(cache: KV4Cache, slots: torch.Tensor, k_out: torch.Tensor | None = None,
              v_out: torch.Tensor | None = None):
     """The cached keys and values of slots [B, L] as bf16 [B, L, Hkv, 128] (zeros for negative slots)."""
+    made = fast().kv4_load(cache.data, cache.page_size, cache.k_scale, cache.v_scale, slots, k_out, v_out)
+    if made is not None:
+        return _made(made, "kv4_load")
     c = cache.c()
     if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
         raise TypeError("slots: expected a contiguous int32 CUDA tensor [B, L]")
@@ -563,6 +590,10 @@ def kv4_attend(Q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, lens
     """Attention of new tokens Q [B, Lq, Hq, 128] over the cached keys and values of their requests: query t of
     request b is at position starts[b] + t (lens[b] - Lq + t without starts) and sees the keys up to its own, with
     window > 0 only the last `window` of them and the first `sinks`."""
+    made = fast().kv4_attend(cache.data, cache.page_size, cache.k_scale, cache.v_scale, Q, block_table, lens, starts, window,
+                             sinks, softmax_scale, out, return_lse, workspace)
+    if made is not None:
+        return _made(made, "kv4_attend")
     tq, c = _b(Q, "Q"), cache.c()
     dev = Q.device
     B, Lq, Hq, D = Q.shape

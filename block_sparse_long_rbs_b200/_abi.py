@@ -123,6 +123,31 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+FASTCALL_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_fastcall.so")
+_fast = None
+
+
+def fast():
+    """The marshalling module of the serving calls, bound to the loaded library (raises if it is not built)."""
+    global _fast
+    if _fast is None:
+        import importlib.machinery
+        import importlib.util
+
+        L = lib()
+        if not os.path.exists(FASTCALL_PATH):
+            raise ImportError(f"_fastcall.so not built at {FASTCALL_PATH}; run python -m block_sparse_long_rbs_b200.build")
+        name = __package__ + "._fastcall"
+        loader = importlib.machinery.ExtensionFileLoader(name, FASTCALL_PATH)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, FASTCALL_PATH, loader=loader))
+        loader.exec_module(m)
+        m.bind(*(ctypes.cast(getattr(L, f), vp).value for f in
+                 ("rope_qk_norm", "swa_prefill", "kv4_extend", "kv4_append", "kv4_load", "kv4_attend",
+                  "rbs_kv4_attend_workspace_bytes")))
+        _fast = m
+    return _fast
+
+
 def check(status: int, where: str) -> None:
     if status != RBS_OK:
         raise RbsError(status, where, lib().rbs_last_error().decode())

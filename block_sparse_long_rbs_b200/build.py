@@ -1,4 +1,5 @@
-"""Build librbs.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build librbs.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_fastcall.so (the serving calls' argument marshalling) with the host compiler.
 
 Usage: python -m block_sparse_long_rbs_b200.build [--force] [--verbose]
 """
@@ -11,12 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librbs.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -46,8 +49,34 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
+def build_fastcall(force: bool = False, verbose: bool = False) -> str:
+    """Compile _fastcall.so (against the installed torch) if its source is newer than it; return its path."""
+    srcs = [os.path.join(CSRC, "fastcall.cpp"), os.path.join(INCLUDE, "rbs.h")]
+    if not force and os.path.exists(FASTCALL) and all(
+            os.path.getmtime(s) <= os.path.getmtime(FASTCALL) for s in srcs):
+        return FASTCALL
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", cuda, "-I", sysconfig.get_paths()["include"], "-o", FASTCALL + ".tmp", srcs[0],
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda",
+           "-lc10"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("compiling fastcall.cpp failed:\n" + res.stdout + res.stderr)
+    os.replace(FASTCALL + ".tmp", FASTCALL)
+    return FASTCALL
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile librbs.so if any source is newer than it; return its path."""
+    """Compile librbs.so and _fastcall.so if a source is newer than they are; return librbs.so's path."""
+    build_fastcall(force, verbose)
     if not force and up_to_date():
         return LIB
     cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, *(extra or []), "-o", LIB + ".tmp",

@@ -181,3 +181,25 @@ def test_binding_refuses_shapes_and_types():
         rbs._table(wide.t(), "t", dev, 8)
     with pytest.raises(ValueError, match="rows"):
         rbs._table(wide, "t", dev, 3)
+
+
+def test_native_marshalling_leaves_odd_arguments_alone(L):
+    """What is not plainly a call's argument (host tensors, other types, wrong counts) comes back as None, undone."""
+    f = _abi.fast()
+    q = torch.zeros(1, 2, 4, 128, dtype=torch.bfloat16)
+    i, data = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(3, 4, 2304, dtype=torch.uint8)
+    assert f.rope_qk_norm(q, q, None, None, i, 1e4, 1e-6, 0, None, None) is None
+    assert f.rope_qk_norm(q, "k", None, None, i, 1e4, 1e-6, 0, None, None) is None
+    assert f.rope_qk_norm(q, q) is None
+    assert f.swa_prefill(q, q, q, 4, 0, 0, None, None, False) is None
+    assert f.swa_prefill(q, q, q, 4, 0, 0, None, None, "yes") is None
+    assert f.kv4_extend(i, i[0, :1], i[0, :1], i[0], i[0, :1], 1, 16, None, None, None) is None
+    assert f.kv4_append(data, 16, 1.0, 1.0, q, q, i) is None
+    assert f.kv4_append([], 16, 1.0, 1.0, q, q, i) is None
+    assert f.kv4_load(data, 16, 1.0, 1.0, i, None, None) is None
+    assert f.kv4_attend(data, 16, 1.0, 1.0, q, i, i[0, :1], None, 0, 0, None, None, True, None) is None
+    assert f.kv4_attend() is None
+    with pytest.raises(TypeError, match="seven"):
+        f.bind(1, 2)
+    with pytest.raises(ValueError, match="null"):
+        f.bind(*[0] * 7)
