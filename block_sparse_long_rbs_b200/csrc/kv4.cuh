@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kExtThreads) kv4_extend_kernel(const __grid_co
         const int e = p / a.page;
         const int32_t pg = e < had ? row[e] : free_page(f + e - had);
         pos = p;
-        if (pg >= 0) slot = pg * a.page + (p - e * a.page);
+        // (an entry that is no page of any cache gives no slot)
+        if (pg >= 0 && pg <= (INT32_MAX - a.page) / a.page) slot = pg * a.page + (p - e * a.page);
       }
       a.slots[static_cast<int64_t>(b) * a.max_new + i] = slot;
       a.pos[static_cast<int64_t>(b) * a.max_new + i] = pos;

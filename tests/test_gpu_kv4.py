@@ -162,6 +162,14 @@ def test_extend_errors(cuda_ok):
         assert (slots >= 0).sum(1).tolist() == want
 
 
+def test_extend_entries_that_are_no_pages(cuda_ok):
+    """An entry whose slots would pass 2^31 - 1 gives none, in the table as held and in the free list."""
+    top = (2 ** 31 - 1 - 16) // 16
+    table = ints([[top + 1, -1], [2 ** 31 - 1, -1], [top, -1], [5, -1]])
+    slots, pos, _ = rbs.kv4_extend(table, ints([3, 3, 3, 16]), ints([4, 4, 4, 17]), ints([2 ** 31 - 1]), ints([0]), 1, 16)
+    assert slots.cpu().tolist() == [[-1], [-1], [16 * top + 3], [-1]] and pos.cpu().tolist() == [[3], [3], [3], [16]]
+
+
 # ---- attention
 
 
