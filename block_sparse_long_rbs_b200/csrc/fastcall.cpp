@@ -124,10 +124,11 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int dev) {
   return at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
 }
 
-// An output: the given tensor, or `like`'s layout.
+// An output: the given tensor, or one of `like`'s layout (a plain layout is
+// allocated directly, past the dispatcher's 2 us).
 bool output(PyObject* o, const at::Tensor& like, at::Tensor* hold, const at::Tensor** x) {
   if (o == Py_None) {
-    *hold = at::empty_like(like);
+    *hold = like.is_contiguous() ? empty(like.sizes(), at::kBFloat16, like.get_device()) : at::empty_like(like);
     *x = hold;
     return true;
   }

@@ -41,7 +41,8 @@
 // Masked scores are replaced before the softmax, so NaN keys stay out; a NaN or
 // infinite value in a masked place still meets a zero weight in the product.
 // Such a row comes out non-finite and is computed again by its warp from the
-// visible keys alone (window_exact_row), as is a row that is non-finite by right.
+// visible keys alone (window_exact_row), as is a row that a visible value makes
+// non-finite by right.
 // Every mbarrier wait is bounded, as in attention.cuh.
 #pragma once
 
@@ -153,30 +154,53 @@ __device__ __forceinline__ int win_key0(const WinItem& x, int t) {
   return x.lo - (x.merged ? kWinSinkRows : 0) + (t - x.n_sink) * kWinKeys;
 }
 
-// One row from the visible keys alone, by a whole warp: lane l holds and
-// returns dims 4l .. 4l + 3.  Only rows whose fast result is not finite come here.
+// One row from the visible keys alone, by a whole warp, 32 keys at a time: lane
+// l forms the score of key l and returns dims 4l .. 4l + 3 of the output.  Only
+// rows whose scores are fit and whose fast output is not finite come here.
 __device__ __noinline__ uint2 window_exact_row(const WinArgs& a, int b, int kvh, int h, int t) {
   const int lane = threadIdx.x & 31;
   const int p = static_cast<int>(a.q_off) + t, w0 = max(0, p - a.W + 1), hi = min(p, a.Lk - 1);
-  const uint2 qx = *reinterpret_cast<const uint2*>(a.Q + b * a.qb + t * a.qs + h * a.qh + 4 * lane);
-  const float q[4] = {bf16lo(qx.x), bf16hi(qx.x), bf16lo(qx.y), bf16hi(qx.y)};
+  const uint4* qr = reinterpret_cast<const uint4*>(a.Q + b * a.qb + t * a.qs + h * a.qh);
+  const __nv_bfloat16 *kb = a.K + b * a.kb + kvh * a.kh, *vb = a.V + b * a.vb + kvh * a.vh + 4 * lane;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  auto take = [&](int s) {
-    const uint2 kx = *reinterpret_cast<const uint2*>(a.K + b * a.kb + s * a.ks + kvh * a.kh + 4 * lane);
-    float d = q[0] * bf16lo(kx.x) + q[1] * bf16hi(kx.x) + q[2] * bf16lo(kx.y) + q[3] * bf16hi(kx.y);
+  auto take = [&](int s0, int n) {  // keys s0 .. s0 + n - 1, n <= 32
+    float d = -INFINITY;
+    if (lane < n) {
+      const uint4* kr = reinterpret_cast<const uint4*>(kb + (s0 + lane) * a.ks);
+      d = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < 16; ++c) {
+        const uint4 q = __ldg(qr + c), k = __ldg(kr + c);
+        d += bf16lo(q.x) * bf16lo(k.x) + bf16hi(q.x) * bf16hi(k.x) + bf16lo(q.y) * bf16lo(k.y) + bf16hi(q.y) * bf16hi(k.y);
+        d += bf16lo(q.z) * bf16lo(k.z) + bf16hi(q.z) * bf16hi(k.z) + bf16lo(q.w) * bf16lo(k.w) + bf16hi(q.w) * bf16hi(k.w);
+      }
+      d *= a.scale_log2;
+    }
+    float mn = fmaxf(m, d);
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) d += __shfl_xor_sync(0xffffffffu, d, i);
-    d *= a.scale_log2;
-    const float mn = fmaxf(m, d), f = m == -INFINITY ? 0.f : ptx_exp2(m - mn), e = mn == -INFINITY ? (d == -INFINITY ? 0.f : d) : ptx_exp2(d - mn);
-    const uint2 vx = *reinterpret_cast<const uint2*>(a.V + b * a.vb + s * a.vs + kvh * a.vh + 4 * lane);
-    const float v[4] = {bf16lo(vx.x), bf16hi(vx.x), bf16lo(vx.y), bf16hi(vx.y)};
+    for (int i = 16; i > 0; i >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, i));
+    // no key with a score above -inf so far: nothing to scale, no weights
+    const float f = m == -INFINITY ? 0.f : ptx_exp2(m - mn), e = mn == -INFINITY ? 0.f : ptx_exp2(d - mn);
+    float sum = e;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
     m = mn;
-    l = l * f + e;
+    l = l * f + sum;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * f + e * v[i];
+    for (int i = 0; i < 4; ++i) o[i] *= f;
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float w = __shfl_sync(0xffffffffu, e, s);
+      const uint2 vx = __ldg(reinterpret_cast<const uint2*>(vb + (s0 + s) * a.vs));
+      o[0] += w * bf16lo(vx.x);
+      o[1] += w * bf16hi(vx.x);
+      o[2] += w * bf16lo(vx.y);
+      o[3] += w * bf16hi(vx.y);
+    }
   };
-  for (int s = 0; s < min(min(a.S, w0), a.Lk); ++s) take(s);
-  for (int s = w0; s <= hi; ++s) take(s);
+  const int ns = min(min(a.S, w0), a.Lk);
+  for (int s = 0; s < ns; s += 32) take(s, min(32, ns - s));
+  for (int s = w0; s <= hi; s += 32) take(s, min(32, hi + 1 - s));
   const float inv = l == 0.f ? 0.f : 1.f / l;
   return make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
 }
@@ -489,7 +513,8 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
         }
       }
       if (live && a.lse != nullptr) a.lse[lse_at] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f;
-      const bool odd = live && !(fabsf(sum.x + sum.y) < INFINITY);
+      // (a NaN in l is a visible score's: the whole row is NaN by right)
+      const bool odd = live && l == l && !(fabsf(sum.x + sum.y) < INFINITY);
       for (uint32_t bad = __ballot_sync(0xffffffffu, odd); bad != 0; bad &= bad - 1) {
         const int src = __ffs(bad) - 1;
         const uint2 y = window_exact_row(a, x.b, x.kvh, __shfl_sync(0xffffffffu, h, src), __shfl_sync(0xffffffffu, t_row, src));

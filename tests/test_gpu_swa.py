@@ -137,6 +137,24 @@ def test_nan_and_infinity_in_masked_places(cuda_ok, G):
         assert np.array_equal(f64(lse)[0, h, ~bad_k], f64(wlse)[0, h, ~bad_k])
 
 
+def test_values_that_spoil_every_row_of_a_long_prompt(cuda_ok):
+    """Rows made again one by one, all 12,000 keys of each, stay far inside the waits' limit."""
+    rng = np.random.default_rng(44)
+    Q, K, V = _qkv(rng, 1, 12000, 8, 1)
+    want, wlse = rbs.swa_prefill(Q, K, V, 0, return_lse=True)
+    V[0, 0, 0, 3] = float("nan")
+    V[0, 1, 0, 4] = float("-inf")
+    rbs.rbs_get_device_error()
+    o, lse = rbs.swa_prefill(Q, K, V, 0, return_lse=True)
+    assert rbs.rbs_get_device_error() == 0
+    assert torch.isnan(o[..., 3]).all() and torch.isneginf(o[:, 1:, :, 4]).all() and torch.isfinite(o[:, 0, :, 4]).all()
+    o[..., 3:5] = want[..., 3:5]
+    # P's rounding here and there (2^-9 of values whose weighted mean size is below 1), the output's twice
+    assert (f64(o) - f64(want) <= 2 * BF16 * np.abs(f64(want)) + 2.0 ** -6).all()
+    assert (f64(want) - f64(o) <= 2 * BF16 * np.abs(f64(want)) + 2.0 ** -6).all()
+    assert torch.equal(lse, wlse)
+
+
 def test_batches_far_apart(cuda_ok):
     """Batch entries more than 2^31 bytes apart (views of one buffer)."""
     rng = np.random.default_rng(35)
