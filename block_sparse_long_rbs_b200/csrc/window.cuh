@@ -31,12 +31,19 @@
 // overlap them with only part of their other work (1890 cycles per pair of
 // tiles measured; the products need 1280: 48 cycles per K = 16 step of S at
 // N = 64, where shared memory is the limit, and 64 of P V).  Measured and left,
-// 16,384 tokens, window 4096, 32 q / 4 KV heads, 892 us as here (1030 us when
+// 16,384 tokens, window 4096, 32 q / 4 KV heads, 890 us as here (1000 us when
 // repeated until the power limit lowers the clock): one CTA with two row tiles on
 // shared key tiles (1056 us: the two run in step, and their exponentials
 // collide), key tiles of 128 in that form (1120 us), a quarter of the
 // exponentials as a polynomial (915 us), two warps per row with the maximum
 // agreed between them (1005 us).
+// A narrow window is bound by what an item costs beside its tiles: 65,536
+// tokens, window 128, 16,384 items of three tiles: 380 us (443 while the 128
+// registers a thread may have did not suffice and 28 bytes were spilled; the
+// outputs' way to memory was 120 us of that).  Measured and left there: no
+// exponentials for 32 columns that no row of a warp sees (5% slower: spills),
+// stores of each softmax warp's own rows, 32 dims at a time, without warp 7
+// (1% slower on both windows).
 //
 // Masked scores are replaced before the softmax, so NaN keys stay out; a NaN or
 // infinite value in a masked place still meets a zero weight in the product.
@@ -132,8 +139,10 @@ __device__ __forceinline__ int win_div(int n, int d, float inv, int& rem) {
 __device__ __forceinline__ WinItem win_item(const WinArgs& a, int w) {
   WinItem x;
   int i;
-  const int bh = win_div(w, a.nt, a.inv_nt, i);
-  x.b = win_div(bh, a.Hkv, a.inv_hkv, x.kvh);
+  // a token tile's KV heads side by side (against one head after another: 2% off
+  // the wide window, 1% off the narrow one)
+  const int bt = win_div(w, a.Hkv, a.inv_hkv, x.kvh);
+  x.b = win_div(bt, a.nt, a.inv_nt, i);
   x.t0 = (a.nt - 1 - i) * a.T;  // the last tokens, with the most keys, first
   x.p0 = static_cast<int>(a.q_off) + x.t0;
   x.p1 = min(x.p0 + a.T, static_cast<int>(a.q_off) + a.Lq) - 1;
@@ -386,22 +395,23 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(k));
     };
-    uint32_t g = 0, it = 0, ns = 0;  // tiles, items, halves of outputs staged
+    uint32_t g = 0, it = 0;  // tiles, items
     bool ok = true;
     for (int w = blockIdx.x; w < a.items && ok; w += gridDim.x) {
       const WinItem x = win_item(a, w);
       const int t_row = x.t0 + tl, h = x.kvh * a.G + gh;
       const bool live = tl < a.T && t_row < a.Lq;
-      const int64_t lse_at = (static_cast<int64_t>(x.b) * a.G * a.Hkv + h) * a.Lq + t_row;
+      auto write_lse = [&](float z) {
+        if (live && a.lse != nullptr) a.lse[(static_cast<int64_t>(x.b) * a.G * a.Hkv + h) * a.Lq + t_row] = z;
+      };
       if (x.n == 0) {
         if (live) {
           uint4* dst = reinterpret_cast<uint4*>(a.O + x.b * a.ob + t_row * a.os + h * a.oh);
           for (int k = 0; k < 16; ++k) dst[k] = make_uint4(0, 0, 0, 0);
-          if (a.lse != nullptr) a.lse[lse_at] = -INFINITY;
         }
+        write_lse(-INFINITY);
         continue;
       }
-      const int p = x.p0 + tl, hi = min(p, a.Lk - 1), w_lo = p - a.W + 1;
       float m_used = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       for (int t = 0; t < x.n; ++t, ++g) {
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
         const bool sink_tile = t < x.n_sink, shared = t == 0 && x.merged;
         if (sink_tile || shared || k0 + kWinKeys - 1 > min(x.p0, a.Lk - 1) || k0 <= x.p1 - a.W) {
           // columns are seen up to hi_c from lo_c on, and below sk_c (sinks): a bit per column
-          const int hi_c = hi - k0, lo_c = sink_tile ? kWinKeys : w_lo - k0;
+          const int p = x.p0 + tl, hi_c = min(p, a.Lk - 1) - k0, lo_c = sink_tile ? kWinKeys : p - a.W + 1 - k0;
           const int sk_c = sink_tile ? x.sinks - k0 : shared ? x.sinks : a.S - k0;
           auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };  // columns 0 .. n - 1
           const unsigned long long see = below(hi_c + 1) & (~below(lo_c) | below(sk_c));
@@ -512,27 +522,29 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
           }
         }
       }
-      if (live && a.lse != nullptr) a.lse[lse_at] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f;
+      write_lse(l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f);
       // (a NaN in l is a visible score's: the whole row is NaN by right)
       const bool odd = live && l == l && !(fabsf(sum.x + sum.y) < INFINITY);
-      for (uint32_t bad = __ballot_sync(0xffffffffu, odd); bad != 0; bad &= bad - 1) {
-        const int src = __ffs(bad) - 1;
-        const uint2 y = window_exact_row(a, x.b, x.kvh, __shfl_sync(0xffffffffu, h, src), __shfl_sync(0xffffffffu, t_row, src));
-#pragma unroll
-        for (int e = 0; e < 64; ++e) {  // pair e is in lane e / 2
-          const uint32_t z = __shfl_sync(0xffffffffu, (e & 1) ? y.y : y.x, e >> 1);
-          if (lane == src) ow[e >> 5][e & 31] = z;
-        }
-      }
+      const uint32_t odd_rows = __ballot_sync(0xffffffffu, odd);
       // 64 dims at a time through the staging buffer, whose stores warp 7 issues
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf, ++ns) {
-        if (ns >= 1 && !__all_sync(0xffffffffu, mbar_wait(bar(kWbStoreEmpty), (ns - 1) & 1, abort_flag, limit))) { ok = false; break; }
+      for (int hf = 0; hf < 2; ++hf) {
+        // the buffer's previous half (two phases per item) has been read
+        if (it + hf >= 1 && !__all_sync(0xffffffffu, mbar_wait(bar(kWbStoreEmpty), (hf + 1) & 1, abort_flag, limit))) { ok = false; break; }
         if (tl < a.T) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sbase + L::kO + ro * 128 + ((k ^ (ro & 7)) << 4)),
                          "r"(ow[hf][4 * k]), "r"(ow[hf][4 * k + 1]), "r"(ow[hf][4 * k + 2]), "r"(ow[hf][4 * k + 3])
+                         : "memory");
+        }
+        for (uint32_t bad = odd_rows; bad != 0; bad &= bad - 1) {
+          const int src = __ffs(bad) - 1, rs = __shfl_sync(0xffffffffu, ro, src);
+          const uint2 y = window_exact_row(a, x.b, x.kvh, __shfl_sync(0xffffffffu, h, src), __shfl_sync(0xffffffffu, t_row, src));
+          __syncwarp();  // over what the row's thread staged
+          if (lane >> 4 == hf)
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sbase + L::kO + rs * 128 + ((((lane & 15) >> 1) ^ (rs & 7)) << 4) + (lane & 1) * 8),
+                         "r"(y.x), "r"(y.y)
                          : "memory");
         }
         fence_proxy_async_smem();
