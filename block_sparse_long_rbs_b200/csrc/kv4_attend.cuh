@@ -37,11 +37,14 @@
 // instructions) with four warps per scheduler.  32 rows per tile: the outputs
 // take 128 registers of every thread, one CTA per SM and two warps per
 // scheduler are left, and latency bounds it (four drafted tokens of four requests
-// of up to 131,072 tokens: 134 us).  Measured and left: tiles of 16 rows
+// of up to 131,072 tokens: 125 us).  Measured and left: tiles of 16 rows
 // there, reading the cache twice (226 against 165 us); pairs of warps that share
 // a sub-block's rows and dims (178 against 133 us: keys converted twice); rings of
 // 4 and 6 stages (120 and 118 us for the 64 requests); two chains of products
-// for the scores (no change).
+// for the scores (no change); groups of four warps that each form the scores of
+// their own sub-block and a quarter of the dims of all four, P going through
+// shared memory, which doubles the warps (138 against 134 us: 634 warp
+// instructions per sub-block for 437).
 #pragma once
 
 #include <type_traits>
@@ -199,7 +202,8 @@ struct AttSmem {
   static constexpr int kQExp = kQ + 8 * NT * 256;                        // float [8 NT]: the rows' powers of two
   // a warp's part for joining, float [8 rows][128 + 4], lies over its own ring
   static_assert(kAttStages * kSubBytes >= 8 * 132 * 4, "the ring holds it");
-  static constexpr int kML = kQExp + 8 * NT * 4;                         // float [8 warps][8 NT][2]
+  static constexpr int kPos = kQExp + 8 * NT * 4;                        // int [8 NT]: the rows' positions, -1: it sees nothing
+  static constexpr int kML = kPos + 8 * NT * 4;                          // float [8 warps][8 NT][2]
   static constexpr int kSums = kML + kAttWarps * 8 * NT * 8;             // int64 [warps]
   static constexpr int kPrefix = kSums + kAttWarps * 8;                  // int32 [B + 1]
   static constexpr int bytes(int B) { return kPrefix + (B + 1) * 4; }
@@ -210,9 +214,14 @@ template <int NT, bool ONE>
 __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kernel(const __grid_constant__ Kv4AttArgs a) {
   using L = AttSmem<NT>;
   constexpr int R = 8 * NT;  // rows of a tile
+  // The next scores beside the products hide latency; 16 rows have no registers
+  // for both and would spill (64 requests of two tokens: 173 us one after the
+  // other, 195 beside).
+  constexpr bool kAhead = NT != 2;
   extern __shared__ __align__(16) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   float* qexp = reinterpret_cast<float*>(smem + L::kQExp);
+  int* qpos = reinterpret_cast<int*>(smem + L::kPos);
   float* ml = reinterpret_cast<float*>(smem + L::kML);
   int64_t* sums = reinterpret_cast<int64_t*>(smem + L::kSums);
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L::kPrefix);
@@ -312,22 +321,22 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
       // pair k, k + 1 belongs to lane (n % 8, (k % 8) / 2), word k / 8
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + ((k0 & 7) >> 1) * 8 + (k0 >> 3) * 4), "r"(w0) : "memory");
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (((k0 + 2) & 7) >> 1) * 8 + (k0 >> 3) * 4), "r"(w1) : "memory");
-      if (lane == 0) qexp[n] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      if (lane == 0) {
+        qexp[n] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const int p = row < rows ? rg.first_q + row / a.G : -1;
+        qpos[n] = p < rg.len ? p : -1;
+      }
     }
     __syncthreads();
 
     // ---- this thread's columns of S^T: rows 8 nt + 2j + {0, 1}
     float sc[NT][2];
-    int qp[NT][2];
     float m_run[NT][2], l_run[NT][2], o[8][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int n = 8 * nt + 2 * j + i, row = row0 + n;
-        sc[nt][i] = a.scale_log2 * qexp[n];
-        const int p = row < rows ? rg.first_q + row / a.G : -1;
-        qp[nt][i] = p < rg.len ? p : -1;  // -1: the row sees nothing
+        sc[nt][i] = a.scale_log2 * qexp[8 * nt + 2 * j + i];
         m_run[nt][i] = kAttNoMax;
         l_run[nt][i] = 0.f;
       }
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int key = tok0 + r + 8 * (q >> 1), p = qp[nt][q & 1];
+            const int key = tok0 + r + 8 * (q >> 1), p = qpos[8 * nt + 2 * j + (q & 1)];
             const bool see = valid && key <= p && (a.window == 0 || key > p - a.window || key < a.sinks);
             if (!see) c[nt][q] = -INFINITY;
           }
@@ -515,10 +524,11 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
             ta = make_uint4(ta.x & ka, ta.y & ka, ta.z & ka, ta.w & ka);
             tb = make_uint4(tb.x & kb, tb.y & kb, tb.z & kb, tb.w & kb);
           }
-          scores(nx, c);
+          if (kAhead) scores(nx, c);
           product(std::false_type{}, st, ta, tb, 0);
+          if (!kAhead) scores(nx, c);
         } else {
-          scores(nx, c);
+          if (kAhead) scores(nx, c);
           if (full) {
             product(std::false_type{}, st, ta, tb, 0);
           } else {
@@ -529,6 +539,7 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
                       make_uint4(tb.x & kb, tb.y & kb, tb.z & kb, tb.w & kb), t);
             }
           }
+          if (!kAhead) scores(nx, c);
         }
         if (v + kAttWarps < v_end) weights(c, v + kAttWarps, (taken >> (kAttStages - 2)) & 1u);
         st = nx;
