@@ -38,6 +38,12 @@ decltype(&kv4_load) p_kv4_load;
 decltype(&kv4_attend) p_kv4_attend;
 decltype(&rbs_kv4_attend_workspace_bytes) p_kv4_attend_workspace_bytes;
 
+// Other Python threads run while an allocation or a launch may block.
+struct NoGil {
+  PyThreadState* state = PyEval_SaveThread();
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
 // A [B, L, H, D] bf16 tensor on `dev` with a contiguous last dimension.
@@ -121,6 +127,7 @@ bool cache(PyObject* const* a, int dev, rbs_kv4_cache* c) {
 rbs_stream_t stream(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int dev) {
+  NoGil g;
   return at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
 }
 
@@ -128,7 +135,12 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int dev) {
 // allocated directly, past the dispatcher's 2 us).
 bool output(PyObject* o, const at::Tensor& like, at::Tensor* hold, const at::Tensor** x) {
   if (o == Py_None) {
-    *hold = like.is_contiguous() ? empty(like.sizes(), at::kBFloat16, like.get_device()) : at::empty_like(like);
+    if (like.is_contiguous()) {
+      *hold = empty(like.sizes(), at::kBFloat16, like.get_device());
+    } else {
+      NoGil g;
+      *hold = at::empty_like(like);
+    }
     *x = hold;
     return true;
   }
@@ -152,7 +164,14 @@ PyObject* tuple(std::initializer_list<PyObject*> items) {
   Py_XDECREF(t);
   return nullptr;
 }
-PyObject* done(rbs_status st, PyObject* outputs) {
+template <class F>
+PyObject* done(F call, PyObject* outputs) {
+  if (outputs == nullptr) return nullptr;
+  rbs_status st;
+  {
+    NoGil g;
+    st = call();
+  }
   if (st == RBS_OK) return outputs;
   Py_DECREF(outputs);
   return PyLong_FromLong(st);
@@ -188,9 +207,8 @@ PyObject* fast_rope(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor *xq, *xk;
   if (!output(a[8], *Q, &hq, &xq) || !output(a[9], *K, &hk, &xk) || !bf16(xq, dev, &qo) || !bf16(xk, dev, &ko)) return nullptr;
   PyObject* r = tuple({give(a[8], hq), give(a[9], hk)});
-  if (r == nullptr) return nullptr;
-  return done(p_rope_qk_norm(&q, &qo, &k, &ko, wq, wk, eps, static_cast<const int32_t*>(pos->data_ptr()),
-                             shared ? 0 : q.seqlen, theta, static_cast<int32_t>(style), stream(dev)),
+  return done([&] { return p_rope_qk_norm(&q, &qo, &k, &ko, wq, wk, eps, static_cast<const int32_t*>(pos->data_ptr()),
+                             shared ? 0 : q.seqlen, theta, static_cast<int32_t>(style), stream(dev)); },
               r);
 }
 
@@ -210,9 +228,8 @@ PyObject* fast_swa(PyObject* const* a, Py_ssize_t n) {
   if (!output(a[7], *Q, &ho, &xo) || !bf16(xo, dev, &o)) return nullptr;
   if (with_lse) lse = empty({q.batch, q.heads, q.seqlen}, at::kFloat, dev);
   PyObject* r = with_lse ? tuple({give(a[7], ho), THPVariable_Wrap(lse)}) : give(a[7], ho);
-  if (r == nullptr) return nullptr;
-  return done(p_swa_prefill(&q, &k, &v, static_cast<int32_t>(window), static_cast<int32_t>(sinks), off, scale, &o,
-                            with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, stream(dev)),
+  return done([&] { return p_swa_prefill(&q, &k, &v, static_cast<int32_t>(window), static_cast<int32_t>(sinks), off, scale, &o,
+                            with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, stream(dev)); },
               r);
 }
 
@@ -239,10 +256,9 @@ PyObject* fast_extend(PyObject* const* a, Py_ssize_t n) {
   }
   auto p = [](const at::Tensor* y) { return static_cast<int32_t*>(y->data_ptr()); };
   PyObject* r = tuple({give(a[7], made[0]), give(a[8], made[1]), give(a[9], made[2])});
-  if (r == nullptr) return nullptr;
-  return done(p_kv4_extend(p(t), stride, static_cast<int32_t>(B), static_cast<int32_t>(t->size(1)), p(old_lens), p(new_lens),
+  return done([&] { return p_kv4_extend(p(t), stride, static_cast<int32_t>(B), static_cast<int32_t>(t->size(1)), p(old_lens), p(new_lens),
                            p(free), free->size(0), p(head), static_cast<int32_t>(page), static_cast<int32_t>(max_new), p(x[0]),
-                           p(x[1]), p(x[2]), stream(dev)),
+                           p(x[1]), p(x[2]), stream(dev)); },
               r);
 }
 
@@ -255,8 +271,7 @@ PyObject* fast_append(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor* slots = tensor(a[6]);
   if (!ints(slots, dev, {k.batch, k.seqlen})) return nullptr;
   PyObject* r = PyLong_FromLong(RBS_OK);
-  if (r == nullptr) return nullptr;
-  return done(p_kv4_append(&c, &k, &v, static_cast<const int32_t*>(slots->data_ptr()), stream(dev)), r);
+  return done([&] { return p_kv4_append(&c, &k, &v, static_cast<const int32_t*>(slots->data_ptr()), stream(dev)); }, r);
 }
 
 // (data, page_size, k_scale, v_scale, slots, k_out, v_out)
@@ -274,8 +289,7 @@ PyObject* fast_load(PyObject* const* a, Py_ssize_t n) {
   }
   if (!bf16(x[0], dev, &k) || !bf16(x[1], dev, &v) || !ints(slots, dev, {k.batch, k.seqlen})) return nullptr;
   PyObject* r = tuple({give(a[5], made[0]), give(a[6], made[1])});
-  if (r == nullptr) return nullptr;
-  return done(p_kv4_load(&c, static_cast<const int32_t*>(slots->data_ptr()), &k, &v, stream(dev)), r);
+  return done([&] { return p_kv4_load(&c, static_cast<const int32_t*>(slots->data_ptr()), &k, &v, stream(dev)); }, r);
 }
 
 // (data, page_size, k_scale, v_scale, Q, block_table, lens, starts, window, sinks, softmax_scale, out, return_lse, workspace)
@@ -303,13 +317,12 @@ PyObject* fast_attend(PyObject* const* a, Py_ssize_t n) {
   if (ws == nullptr || !ws->is_cuda() || ws->get_device() != dev || ws->scalar_type() != at::kByte || !ws->is_contiguous())
     return nullptr;
   PyObject* r = with_lse ? tuple({give(a[11], ho), THPVariable_Wrap(lse)}) : give(a[11], ho);
-  if (r == nullptr) return nullptr;
-  return done(p_kv4_attend(&q, &c, static_cast<const int32_t*>(t->data_ptr()), stride, static_cast<int32_t>(t->size(1)),
+  return done([&] { return p_kv4_attend(&q, &c, static_cast<const int32_t*>(t->data_ptr()), stride, static_cast<int32_t>(t->size(1)),
                            static_cast<const int32_t*>(lens->data_ptr()),
                            starts == nullptr ? nullptr : static_cast<const int32_t*>(starts->data_ptr()),
                            static_cast<int32_t>(window), static_cast<int32_t>(sinks), scale, ws->data_ptr(),
                            static_cast<size_t>(ws->numel()), &o, with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
-                           stream(dev)),
+                           stream(dev)); },
               r);
 }
 

@@ -127,3 +127,39 @@ def test_same_errors(cuda_ok):
                     f()
             finally:
                 rbs.fast = real
+
+
+def test_threads(cuda_ok):
+    """Calls from several threads at once, each on its own stream."""
+    import threading
+
+    rng = np.random.default_rng(4)
+    cache, table = rbs.KV4Cache.empty(8, 16, 2), ints(np.arange(8).reshape(2, 4))
+    K = randn(rng, 2, 64, 2, 128)
+    rbs.kv4_append(cache, K, K, ints(np.arange(128).reshape(2, 64)))
+    Q = [randn(rng, 2, 3, 8, 128) for _ in range(4)]
+    lens, pos = ints([64, 50]), ints([7, 8, 9])
+
+    def chain(q):
+        x, _ = rbs.rope_qk_norm(q, K[:, :3], None, None, pos, 1e4)
+        return rbs.kv4_attend(x, cache, table, lens, return_lse=True)
+    want = [chain(q) for q in Q]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    o, z = chain(Q[i])
+                    torch.cuda.current_stream().synchronize()
+                    if not (torch.equal(o, want[i][0]) and torch.equal(z, want[i][1])):
+                        wrong.append(i)
+        except Exception as e:  # a thread's own would be lost
+            wrong.append(e)
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not wrong
