@@ -32,7 +32,7 @@
 // may not see set to zero.
 // 144 bytes per cached token and KV head have to be read.  Measured: 64 requests of
 // 8,192 to 16,384 tokens, 32 q / 4 KV heads (about 456 MB): 117 us, 3.9 TB/s of the
-// 6.46 a copy reaches; bound by instruction issue (63% of the slots, about 400 warp
+// 6.46 a copy reaches; bound by instruction issue (60% of the slots, about 400 warp
 // instructions per sub-block, of them 88 conversions, 64 scalings, 16 matrix
 // instructions) with four warps per scheduler.  32 rows per tile: the outputs
 // take 128 registers of every thread, one CTA per SM and two warps per
