@@ -15,8 +15,7 @@
 // kv4_combine_kernel joins them in their order, so results do not vary.
 //
 // A warp works on its own sub-blocks with no barrier: 2304 bytes by 16-byte
-// asynchronous copies into its ring, then, the first product of a sub-block
-// beside the second one of the sub-block before,
+// asynchronous copies into its ring, then
 //   S^T (16 keys x 8 rows) = K Q^T,  O^T (16 dims x 8 rows) += V^T P^T
 // by mma.m16n8k16 in fp16 with fp32 sums: rows of queries are the instruction's
 // narrow side, since one token's G rows rarely fill the wide one.  The codes
@@ -31,20 +30,22 @@
 // taken once per query token, for that token's rows alone and with the keys it
 // may not see set to zero.
 // 144 bytes per cached token and KV head have to be read.  Measured: 64 requests of
-// 8,192 to 16,384 tokens, 32 q / 4 KV heads (about 456 MB): 117 us, 3.9 TB/s of the
+// 8,192 to 16,384 tokens, 32 q / 4 KV heads (about 456 MB): 118 us, 3.9 TB/s of the
 // 6.46 a copy reaches; bound by instruction issue (60% of the slots, about 400 warp
 // instructions per sub-block, of them 88 conversions, 64 scalings, 16 matrix
 // instructions) with four warps per scheduler.  32 rows per tile: the outputs
 // take 128 registers of every thread, one CTA per SM and two warps per
 // scheduler are left, and latency bounds it (four drafted tokens of four requests
-// of up to 131,072 tokens: 125 us).  Measured and left: tiles of 16 rows
+// of up to 131,072 tokens: 122 us).  Measured and left: tiles of 16 rows
 // there, reading the cache twice (226 against 165 us); pairs of warps that share
 // a sub-block's rows and dims (178 against 133 us: keys converted twice); rings of
 // 4 and 6 stages (120 and 118 us for the 64 requests); two chains of products
-// for the scores (no change); groups of four warps that each form the scores of
-// their own sub-block and a quarter of the dims of all four, P going through
-// shared memory, which doubles the warps (138 against 134 us: 634 warp
-// instructions per sub-block for 437).
+// for the scores (no change); the next sub-block's scores before this one's
+// products (no change, and 16 rows spill: 195 against 173 us for 64 requests of
+// two tokens); groups of four warps that each form the scores of their own
+// sub-block and a quarter of the dims of all four, P going through shared
+// memory, which doubles the warps (138 against 134 us: 634 warp instructions per
+// sub-block for 437).
 #pragma once
 
 #include <type_traits>
@@ -214,10 +215,6 @@ template <int NT, bool ONE>
 __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kernel(const __grid_constant__ Kv4AttArgs a) {
   using L = AttSmem<NT>;
   constexpr int R = 8 * NT;  // rows of a tile
-  // The next scores beside the products hide latency; 16 rows have no registers
-  // for both and would spill (64 requests of two tokens: 173 us one after the
-  // other, 195 beside).
-  constexpr bool kAhead = NT != 2;
   extern __shared__ __align__(16) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   float* qexp = reinterpret_cast<float*>(smem + L::kQExp);
@@ -355,7 +352,7 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
     const int full_lo = a.window == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(max(p_hi - a.window + 1, 0)) + 15u) >> 4) - shift;
     const int full_sink = all_live ? min(rg.sink, a.sinks >> 4) : 0;
 
-    // ---- the sub-blocks: scores of the next one beside the products of this one
+    // ---- the sub-blocks: products of one, then scores of the next
     uint32_t p0[NT], p1[NT];  // P^T, the second product's operand: keys 2j, 2j + 1 (+ 8) of row r
     bool full = true, valid = true;  // of the sub-block whose P these are
     int tok0 = 0;
@@ -517,18 +514,14 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
         issue();
         const uint32_t scales = st + 2176 + 16 * j;
         uint4 ta = lds128(scales), tb = lds128(scales + 64);
-        // (scores past the last sub-block: of whatever the stage holds, unused)
         if (ONE) {
           if (!full) {
             const uint32_t ka = keep(2 * j, rg.first_q), kb = keep(2 * j + 8, rg.first_q);
             ta = make_uint4(ta.x & ka, ta.y & ka, ta.z & ka, ta.w & ka);
             tb = make_uint4(tb.x & kb, tb.y & kb, tb.z & kb, tb.w & kb);
           }
-          if (kAhead) scores(nx, c);
           product(std::false_type{}, st, ta, tb, 0);
-          if (!kAhead) scores(nx, c);
         } else {
-          if (kAhead) scores(nx, c);
           if (full) {
             product(std::false_type{}, st, ta, tb, 0);
           } else {
@@ -539,9 +532,11 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
                       make_uint4(tb.x & kb, tb.y & kb, tb.z & kb, tb.w & kb), t);
             }
           }
-          if (!kAhead) scores(nx, c);
         }
-        if (v + kAttWarps < v_end) weights(c, v + kAttWarps, (taken >> (kAttStages - 2)) & 1u);
+        if (v + kAttWarps < v_end) {
+          scores(nx, c);
+          weights(c, v + kAttWarps, (taken >> (kAttStages - 2)) & 1u);
+        }
         st = nx;
         nx = nx == ring + (kAttStages - 1) * kSubBytes ? ring : nx + kSubBytes;
       }
