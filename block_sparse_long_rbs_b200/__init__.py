@@ -13,6 +13,7 @@ import ctypes
 import dataclasses
 import functools
 import math
+import operator
 
 import torch
 
@@ -366,6 +367,34 @@ def _made(result, where: str):
     return result
 
 
+def _int(x, name: str, bits: int) -> int:
+    """An integer that a signed C integer of that many bits holds (ctypes would cut off the rest)."""
+    try:
+        n = operator.index(x)
+    except TypeError:
+        raise TypeError(f"{name}: expected an integer") from None
+    if not -(1 << bits - 1) <= n < 1 << bits - 1:
+        raise ValueError(f"{name}: {n} does not fit {bits} bits")
+    return n
+
+
+def _i32(x, name: str) -> int:
+    return _int(x, name, 32)
+
+
+def _i64(x, name: str) -> int:
+    return _int(x, name, 64)
+
+
+def _reach(x, name: str) -> int:
+    """A window or a count of sinks: positions end below 2^31, so what lies past that reaches every key as 2^31 - 1 does
+    (and anything negative is left to the library to refuse)."""
+    try:
+        return max(-1, min(operator.index(x), 2 ** 31 - 1))
+    except TypeError:
+        raise TypeError(f"{name}: expected an integer") from None
+
+
 def _b(x, name: str) -> Bf16Tensor:
     """_t with the passing case first."""
     try:
@@ -418,6 +447,7 @@ def _table(x, name: str, dev: torch.device, rows: int) -> tuple[int, int, int]:
         raise ValueError(f"{name}: expected {rows} rows, got {n}")
     if x.device != dev:
         raise ValueError(f"{name} is on {x.device}, expected {dev}: every tensor of a call must be on one device")
+    _i32(n, f"rows of {name}"), _i32(width, f"width of {name}")
     return x.data_ptr(), stride if rows > 1 else max(stride, width), width
 
 
@@ -429,6 +459,7 @@ def rope_qk_norm(Q: torch.Tensor, K: torch.Tensor, q_weight: torch.Tensor | None
     made = fast().rope_qk_norm(Q, K, q_weight, k_weight, pos, theta, eps, rope_style, q_out, k_out)
     if made is not None:
         return _made(made, "rope_qk_norm")
+    rope_style = _i32(rope_style, "rope_style")
     if q_out is None:
         q_out = torch.empty_like(Q)
     if k_out is None:
@@ -462,6 +493,7 @@ def swa_prefill(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, window: int, 
     made = fast().swa_prefill(Q, K, V, window, sinks, q_offset, softmax_scale, out, return_lse)
     if made is not None:
         return _made(made, "swa_prefill")
+    window, sinks, q_offset = _reach(window, "window"), _reach(sinks, "sinks"), _i64(q_offset, "q_offset")
     tq, tk, tv = _b(Q, "Q"), _b(K, "K"), _b(V, "V")
     dev = Q.device
     if out is None:
@@ -478,7 +510,7 @@ def swa_prefill(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, window: int, 
 
 def rbs_kv4_page_bytes(page_size: int) -> int:
     """Bytes of one page of one KV head of the 4-bit cache."""
-    n = int(lib().rbs_kv4_page_bytes(page_size))
+    n = int(lib().rbs_kv4_page_bytes(_i32(page_size, "page_size")))
     if n < 0:
         raise RbsError(2, "rbs_kv4_page_bytes", lib().rbs_last_error().decode())
     return n
@@ -506,10 +538,11 @@ class KV4Cache:
         if not x.is_cuda or x.dtype is not torch.uint8 or not x.is_contiguous() or x.dim() != 3:
             raise TypeError("cache.data: expected a contiguous uint8 CUDA tensor [num_pages, Hkv, page bytes]")
         pages, heads, size = x.shape
+        page_size = _i32(self.page_size, "cache.page_size")
         # a page is page_size / 16 sub-blocks of 2304 bytes; the library checks the page size itself
-        if size != self.page_size // 16 * 2304:
-            raise ValueError(f"cache.data: pages of {size} bytes, expected {self.page_size // 16 * 2304}")
-        return KV4CacheC(x.data_ptr(), pages, heads, self.page_size, self.k_scale, self.v_scale)
+        if size != page_size // 16 * 2304:
+            raise ValueError(f"cache.data: pages of {size} bytes, expected {page_size // 16 * 2304}")
+        return KV4CacheC(x.data_ptr(), pages, heads, page_size, self.k_scale, self.v_scale)
 
 
 def kv4_extend(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
@@ -522,6 +555,7 @@ def kv4_extend(block_table: torch.Tensor, old_lens: torch.Tensor, new_lens: torc
                              free_head_out)
     if made is not None:
         return _made(made, "kv4_extend")
+    max_new, page_size = _i32(max_new, "max_new"), _i32(page_size, "page_size")
     if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
         raise TypeError("block_table: expected a CUDA tensor")
     dev, B = block_table.device, block_table.shape[0]
@@ -580,7 +614,8 @@ def kv4_load(cache: KV4Cache, slots: torch.Tensor, k_out: torch.Tensor | None = 
 
 @functools.lru_cache(maxsize=256)  # a function of the sizes alone
 def rbs_kv4_attend_workspace_bytes(seqlen_q: int, heads_q: int, kv_heads: int) -> int:
-    return int(lib().rbs_kv4_attend_workspace_bytes(seqlen_q, heads_q, kv_heads))
+    return int(lib().rbs_kv4_attend_workspace_bytes(_i64(seqlen_q, "seqlen_q"), _i64(heads_q, "heads_q"),
+                                                    _i64(kv_heads, "kv_heads")))
 
 
 def kv4_attend(Q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, lens: torch.Tensor,
@@ -594,6 +629,7 @@ def kv4_attend(Q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, lens
                              sinks, softmax_scale, out, return_lse, workspace)
     if made is not None:
         return _made(made, "kv4_attend")
+    window, sinks = _reach(window, "window"), _reach(sinks, "sinks")
     tq, c = _b(Q, "Q"), cache.c()
     dev = Q.device
     B, Lq, Hq, D = Q.shape

@@ -420,3 +420,35 @@ def test_attend_a_prompt(cuda_ok):
     for kw in ({}, dict(window=20, sinks=2)):
         o, lse = _attend(held, Q, **kw)
         _check(o, lse, held, Q, **kw)
+
+
+def test_windows_and_sinks_past_32_bits(cuda_ok):
+    """A window or a count of sinks that no int32 holds is one that reaches every key."""
+    rng = np.random.default_rng(62)
+    held = Held(rng, [200, 90], 2, 32)
+    Q = randn(rng, 2, 3, 4, 128)
+    full, _ = _attend(held, Q)
+    for big in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 128, 2 ** 64 + 5):
+        a, _ = _attend(held, Q, window=big)
+        b, _ = _attend(held, Q, window=3, sinks=big)
+        assert torch.equal(a, full)
+        _check(b, None, held, Q)
+    for bad in (-1, -2 ** 31 - 1, -2 ** 32 + 7, -2 ** 64):
+        for kw in (dict(window=bad), dict(window=4, sinks=bad)):
+            with pytest.raises(rbs.RbsError, match=">= 0"):
+                _attend(held, Q, **kw)
+
+
+def test_integers_past_32_bits_are_refused(cuda_ok):
+    rng = np.random.default_rng(63)
+    K, cache = randn(rng, 1, 4, 2, 128), rbs.KV4Cache.empty(2, 16, 2)
+    table, n = ints([[0]]), ints([1])
+    for bad in (2 ** 31, 2 ** 32 + 16, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="page_size"):
+            rbs.kv4_extend(table, n, n, n, n, 1, bad)
+        with pytest.raises(ValueError, match="max_new"):
+            rbs.kv4_extend(table, n, n, n, n, bad, 16)
+        with pytest.raises(ValueError, match="page_size"):
+            rbs.kv4_load(rbs.KV4Cache(cache.data, bad), n[None])
+        with pytest.raises(ValueError, match="rope_style"):
+            rbs.rope_qk_norm(K, K, None, None, ints(np.arange(4)), 1e4, rope_style=bad)

@@ -187,3 +187,22 @@ def test_wait_that_runs_out_returns_timeout_and_the_next_call_is_correct(cuda_ok
     _check(Q, K, V, 500, 4, rows=np.unique(rng.integers(0, 3000, 40)))
     for wait, n in ((10, 5), (3_000_000_000, 5), (1_000_000, -1)):
         assert L_.rbs_testing_swa_prefill_stalled(*args, wait, n, _t(out, "O"), _stream()) == 1
+
+
+def test_windows_and_sinks_past_32_bits(cuda_ok):
+    """A window or a count of sinks that no int32 holds is one that reaches every key."""
+    rng = np.random.default_rng(47)
+    Q, K, V = _qkv(rng, 1, 200, 4, 2)
+    full = rbs.swa_prefill(Q, K, V, 0)
+    for big in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 128, 2 ** 64 + 5):
+        assert torch.equal(rbs.swa_prefill(Q, K, V, big), full)
+        assert torch.equal(rbs.swa_prefill(Q, K, V, 3, big), full)
+    for bad in (-1, -2 ** 31 - 1, -2 ** 32 + 7, -2 ** 64):
+        with pytest.raises(rbs.RbsError, match=">= 0"):
+            rbs.swa_prefill(Q, K, V, bad)
+        with pytest.raises(rbs.RbsError, match=">= 0"):
+            rbs.swa_prefill(Q, K, V, 4, bad)
+    with pytest.raises(ValueError, match="q_offset"):
+        rbs.swa_prefill(Q, K, V, 4, q_offset=2 ** 64 + 5)
+    with pytest.raises(rbs.RbsError, match="2\\^31"):
+        rbs.swa_prefill(Q, K, V, 4, q_offset=2 ** 32 + 5)

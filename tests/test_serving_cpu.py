@@ -203,3 +203,28 @@ def test_native_marshalling_leaves_odd_arguments_alone(L):
         f.bind(1, 2)
     with pytest.raises(ValueError, match="null"):
         f.bind(*[0] * 7)
+
+
+def test_binding_integers():
+    """Integers that their C type does not hold are refused, and windows and sinks past 32 bits reach every key."""
+    assert rbs._i32(-2 ** 31, "x") == -2 ** 31 and rbs._i32(2 ** 31 - 1, "x") == 2 ** 31 - 1
+    assert rbs._i64(-2 ** 63, "x") == -2 ** 63 and rbs._i64(2 ** 63 - 1, "x") == 2 ** 63 - 1
+    for bad in (2 ** 31, -2 ** 31 - 1, 2 ** 32 + 5, 2 ** 64):
+        with pytest.raises(ValueError, match="x: .* 32 bits"):
+            rbs._i32(bad, "x")
+    for bad in (2 ** 63, -2 ** 63 - 1, 2 ** 64 + 5):
+        with pytest.raises(ValueError, match="x: .* 64 bits"):
+            rbs._i64(bad, "x")
+    for f in (rbs._i32, rbs._i64, rbs._reach):
+        with pytest.raises(TypeError, match="x: expected an integer"):
+            f(4.0, "x")
+    assert [rbs._reach(n, "x") for n in (0, 7, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 128, 2 ** 64)] == [0, 7] + [2 ** 31 - 1] * 4
+    assert all(rbs._reach(n, "x") < 0 for n in (-1, -2 ** 31 - 1, -2 ** 32 + 7, -2 ** 64))  # the library refuses them
+    for bad in (2 ** 32 + 64, -2 ** 32 + 64):
+        with pytest.raises(ValueError, match="page_size"):
+            rbs.rbs_kv4_page_bytes(bad)
+        with pytest.raises(ValueError, match="page_size"):
+            rbs.KV4Cache.empty(1, bad, 1, device="cpu")
+    for sizes in ((2 ** 64 + 1, 8, 2), (1, 2 ** 64 + 8, 2), (1, 8, 2 ** 64 + 2)):
+        with pytest.raises(ValueError, match="64 bits"):
+            rbs.rbs_kv4_attend_workspace_bytes(*sizes)
