@@ -1229,15 +1229,14 @@ rbs_status launch_swa(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const 
   for (int x = 0; x < 2; ++x) {
     const rbs_bf16_tensor* t = x == 0 ? K : V;
     if ((st = make_tensor_map(t, kWinKeys, x == 0 ? &a.tmK : &a.tmV, &si)) != RBS_OK) return st;
-    if ((st = make_tensor_map(t, kWinSinkRows, x == 0 ? &a.tmKs : &a.tmVs, &si)) != RBS_OK) return st;
+    rbs_bf16_tensor first = *t;  // the sinks' values end with them: the rows of a tile past them are zeros
+    if (x == 1) first.seqlen = std::max<int64_t>(1, std::min<int64_t>(sinks, t->seqlen));
+    if ((st = make_tensor_map(&first, kWinSinkRows, x == 0 ? &a.tmKs : &a.tmVs, &si)) != RBS_OK) return st;
+    if (x == 1 && (st = make_tensor_map(&first, kWinKeys, &a.tmVt, &si)) != RBS_OK) return st;
     if ((st = make_tensor_map(t, kWinKeys - kWinSinkRows, x == 0 ? &a.tmKw : &a.tmVw, &si)) != RBS_OK) return st;
   }
-  a.Q = static_cast<const __nv_bfloat16*>(Q->data);
-  a.K = static_cast<const __nv_bfloat16*>(K->data);
   a.V = static_cast<const __nv_bfloat16*>(V->data);
   a.O = static_cast<__nv_bfloat16*>(O->data);
-  a.qb = Q->stride_b; a.qs = Q->stride_s; a.qh = Q->stride_h;
-  a.kb = K->stride_b; a.ks = K->stride_s; a.kh = K->stride_h;
   a.vb = V->stride_b; a.vs = V->stride_s; a.vh = V->stride_h;
   a.ob = O->stride_b; a.os = O->stride_s; a.oh = O->stride_h;
   a.lse = lse;

@@ -45,11 +45,16 @@
 // stores of each softmax warp's own rows, 32 dims at a time, without warp 7
 // (1% slower on both windows).
 //
-// Masked scores are replaced before the softmax, so NaN keys stay out; a NaN or
-// infinite value in a masked place still meets a zero weight in the product.
-// Such a row comes out non-finite and is computed again by its warp from the
-// visible keys alone (window_exact_row), as is a row that a visible value makes
-// non-finite by right.
+// Masked scores are replaced before the softmax, so NaN keys stay out.  A masked
+// value still meets its zero weight in the product, and zero times a NaN or an
+// infinity is NaN.  The keys that some row of an item does not see are few: the
+// window's edges (fewer than T keys each) and what the last tile holds past the
+// last token (the copies fill what lies past the sinks with zeros).  Warp 7
+// looks through those before their product and sets what is not finite there to
+// zero; where it found some, each row adds those that it does see (whatever
+// their weights, they make the sum non-finite) to its outputs at the end.  What
+// this costs depends on T alone, however many values there are and however long
+// the prompt is.
 // Every mbarrier wait is bounded, as in attention.cuh.
 #pragma once
 
@@ -59,10 +64,11 @@ namespace rbs {
 
 struct WinArgs {
   // Q boxes of T tokens x G heads, O's the same (ordered by stride), K / V boxes of 64, 16 and 48 keys
-  CUtensorMap tmQ, tmO, tmK, tmV, tmKs, tmVs, tmKw, tmVw;
-  const __nv_bfloat16 *Q, *K, *V;
+  // tmVs, tmVt (64 keys): values that end with the sinks, zeros past them
+  CUtensorMap tmQ, tmO, tmK, tmV, tmKs, tmVs, tmKw, tmVw, tmVt;
+  const __nv_bfloat16* V;
   __nv_bfloat16* O;
-  int64_t qb, qs, qh, kb, ks, kh, vb, vs, vh, ob, os, oh;
+  int64_t vb, vs, vh, ob, os, oh;
   int o_seq_inner;  // O's token stride is the smaller one: its box is T tokens inside G heads
   float* lse;  // [B, Hq, Lq] or null
   int B, G, Hkv, Lq, Lk, T, nt;  // T tokens per item, nt items per (batch, KV head)
@@ -109,7 +115,8 @@ enum : int {
   kWbOEmpty = kWbOFull + 1,
   kWbStoreFull = kWbOEmpty + 1,  // 64 dims of the outputs are staged
   kWbStoreEmpty = kWbStoreFull + 1,
-  kWbDrain = kWbStoreEmpty + 1,  // + issuer
+  kWbScrubbed = kWbStoreEmpty + 1,  // every tile of the item has been looked through
+  kWbDrain = kWbScrubbed + 1,    // + issuer
   kWbNum = kWbDrain + 2
 };
 static_assert(kWbNum * 8 + 16 <= 256, "barrier area");
@@ -163,55 +170,64 @@ __device__ __forceinline__ int win_key0(const WinItem& x, int t) {
   return x.lo - (x.merged ? kWinSinkRows : 0) + (t - x.n_sink) * kWinKeys;
 }
 
-// One row from the visible keys alone, by a whole warp, 32 keys at a time: lane
-// l forms the score of key l and returns dims 4l .. 4l + 3 of the output.  Only
-// rows whose scores are fit and whose fast output is not finite come here.
-__device__ __noinline__ uint2 window_exact_row(const WinArgs& a, int b, int kvh, int h, int t) {
+// Bit patterns of bf16 pairs that hold a NaN or an infinity.
+__device__ __forceinline__ bool bf16x2_odd(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// Columns [c0, c1) of a value tile in shared memory, by a whole warp: what is not finite becomes zero.
+__device__ __forceinline__ bool window_scrub(uint32_t tile, int c0, int c1) {
   const int lane = threadIdx.x & 31;
-  const int p = static_cast<int>(a.q_off) + t, w0 = max(0, p - a.W + 1), hi = min(p, a.Lk - 1);
-  const uint4* qr = reinterpret_cast<const uint4*>(a.Q + b * a.qb + t * a.qs + h * a.qh);
-  const __nv_bfloat16 *kb = a.K + b * a.kb + kvh * a.kh, *vb = a.V + b * a.vb + kvh * a.vh + 4 * lane;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  auto take = [&](int s0, int n) {  // keys s0 .. s0 + n - 1, n <= 32
-    float d = -INFINITY;
-    if (lane < n) {
-      const uint4* kr = reinterpret_cast<const uint4*>(kb + (s0 + lane) * a.ks);
-      d = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < 16; ++c) {
-        const uint4 q = __ldg(qr + c), k = __ldg(kr + c);
-        d += bf16lo(q.x) * bf16lo(k.x) + bf16hi(q.x) * bf16hi(k.x) + bf16lo(q.y) * bf16lo(k.y) + bf16hi(q.y) * bf16hi(k.y);
-        d += bf16lo(q.z) * bf16lo(k.z) + bf16hi(q.z) * bf16hi(k.z) + bf16lo(q.w) * bf16lo(k.w) + bf16hi(q.w) * bf16hi(k.w);
+  bool found = false;
+#pragma unroll 2
+  for (int c = c0 + (lane >> 3); c < c1; c += 4) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const uint32_t at = tile + hf * (kWinKeys * 128) + c * 128 + (lane & 7) * 16;
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+      uint32_t top = 0;  // the largest size of each half, by its bits
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
+      if (bf16x2_odd(top)) {
+        found = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
+          if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu;
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
       }
-      d *= a.scale_log2;
     }
-    float mn = fmaxf(m, d);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, i));
-    // no key with a score above -inf so far: nothing to scale, no weights
-    const float f = m == -INFINITY ? 0.f : ptx_exp2(m - mn), e = mn == -INFINITY ? 0.f : ptx_exp2(d - mn);
-    float sum = e;
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-    m = mn;
-    l = l * f + sum;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= f;
-#pragma unroll 8
-    for (int s = 0; s < n; ++s) {
-      const float w = __shfl_sync(0xffffffffu, e, s);
-      const uint2 vx = __ldg(reinterpret_cast<const uint2*>(vb + (s0 + s) * a.vs));
-      o[0] += w * bf16lo(vx.x);
-      o[1] += w * bf16hi(vx.x);
-      o[2] += w * bf16lo(vx.y);
-      o[3] += w * bf16hi(vx.y);
+  }
+  return __any_sync(0xffffffffu, found);
+}
+
+// What window_scrub took from the query at position p, back onto 64 dims of its
+// staged outputs, by a whole warp, two dims a lane: v points at the lane's
+// dims of key 0, out at its place in the staged row.
+__device__ __noinline__ void window_restore(const WinArgs& a, const __nv_bfloat16* v, int p, int lo, int p0, int p1, uint32_t out) {
+  float2 add = make_float2(0.f, 0.f);  // of values that are not finite alone
+  auto take = [&](int s0, int s1) {    // keys s0 .. s1
+#pragma unroll 4
+    for (int s = s0; s <= s1; ++s) {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(v + s * a.vs));
+      if ((w & 0x7f80u) == 0x7f80u) add.x += bf16lo(w);
+      if ((w & 0x7f800000u) == 0x7f800000u) add.y += bf16hi(w);
     }
   };
-  const int ns = min(min(a.S, w0), a.Lk);
-  for (int s = 0; s < ns; s += 32) take(s, min(32, ns - s));
-  for (int s = w0; s <= hi; s += 32) take(s, min(32, hi + 1 - s));
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  return make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  // the keys of either edge that the row sees: in its window, then its sinks
+  // among them (a key taken twice changes nothing)
+  const int see = p - a.W + 1, lo_end = min(min(p1 - a.W, p), a.Lk - 1), hi_from = max(lo, p0 + 1), hi_end = min(p, a.Lk - 1);
+  take(max(lo, see), lo_end);
+  take(lo, min(a.S - 1, lo_end));
+  take(max(hi_from, see), hi_end);
+  take(hi_from, min(a.S - 1, hi_end));
+  uint32_t o;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(o) : "r"(out) : "memory");
+  if (add.x != 0.f) o = (o & 0xffff0000u) | (pack_bf16x2(bf16lo(o) + add.x, 0.f) & 0xffffu);
+  if (add.y != 0.f) o = (o & 0xffffu) | (pack_bf16x2(0.f, bf16hi(o) + add.y) & 0xffff0000u);
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(out), "r"(o) : "memory");
 }
 
 __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __grid_constant__ WinArgs a) {
@@ -227,6 +243,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
   auto bar = [&](int k) -> uint32_t { return bars + 8u * k; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBar + kWbNum * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kBar + kWbNum * 8 + 4);
+  volatile int* scrubbed = reinterpret_cast<volatile int*>(smem + L::kBar + kWbNum * 8 + 8);  // the item's tiles held values to take out
   const uint64_t limit = a.wait_ns;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -246,6 +263,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
     mbar_init(bar(kWbOEmpty), 4);
     mbar_init(bar(kWbStoreFull), 4);
     mbar_init(bar(kWbStoreEmpty), 1);
+    mbar_init(bar(kWbScrubbed), 1);
     mbar_init(bar(kWbDrain), 1);
     mbar_init(bar(kWbDrain + 1), 1);
     *abort_flag = 0;
@@ -304,7 +322,10 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
           mbar_arrive_expect_tx(bar(full0 + s), L::kKVBytes);
           const uint32_t dst = ring + s * L::kKVBytes;
           const int k0 = win_key0(x, t);
-          if (t == 0 && x.merged) {
+          if (t < x.n_sink && !isK) {
+            tma_load_4d_hint(dst, &a.tmVt, bar(full0 + s), 0, x.kvh, k0, x.b, pol_kv);
+            tma_load_4d_hint(dst + kWinKeys * 128, &a.tmVt, bar(full0 + s), 64, x.kvh, k0, x.b, pol_kv);
+          } else if (t == 0 && x.merged) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               const uint32_t d = dst + hf * kWinKeys * 128;
@@ -334,7 +355,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
     constexpr uint32_t kStageUnits = L::kKVBytes >> 4, kQHalf = (128 * 128) >> 4, kKHalf = (kWinKeys * 128) >> 4;
     auto wait = [&](int k, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(k), parity, abort_flag, limit)); };
     uint32_t g = 0, it = 0;  // tiles and items so far
-    bool ok = true;
+    bool ok = true, odd = false;
     for (int w = blockIdx.x; w < a.items && ok; w += gridDim.x) {
       const WinItem x = win_item(a, w);
       if (x.n == 0) continue;
@@ -354,8 +375,25 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
           umma_commit_warp(bar(kWbSFull + b));
           if (t == x.n - 1) umma_commit_warp(bar(kWbQEmpty));
         } else {
-          if (!wait(kWbPFull + b, (g >> 1) & 1)) { ok = false; break; }
           if (!wait(kWbVFull + s, (g / kWinNS) & 1)) { ok = false; break; }
+          // the tile's keys that some row does not see, while its weights are
+          // still being formed: at the window's lower edge, and past the first token
+          if (t == 0) odd = false;
+          if (t >= x.n_sink) {
+            const int k0 = win_key0(x, t), c0 = t == 0 && x.merged ? kWinSinkRows : 0;
+            const bool lower = window_scrub(sV + s * L::kKVBytes, c0, min(kWinKeys, x.p1 - a.W + 1 - k0));
+            const bool upper = window_scrub(sV + s * L::kKVBytes, max(c0, x.p0 + 1 - k0), min(kWinKeys, a.Lk - k0));
+            if (lower || upper) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              odd = true;
+            }
+          }
+          if (t == x.n - 1 && lane == 0) {
+            *scrubbed = odd;
+            mbar_arrive(bar(kWbScrubbed));
+          }
+          if (!wait(kWbPFull + b, (g >> 1) & 1)) { ok = false; break; }
           if (t == 0 && it > 0 && !wait(kWbOEmpty, (it - 1) & 1)) { ok = false; break; }
           tc_fence_after();
           const uint64_t vd = vdesc0 + s * kStageUnits;
@@ -499,7 +537,8 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (!__all_sync(0xffffffffu, mbar_wait(bar(kWbOFull), it & 1, abort_flag, limit))) { ok = false; break; }
       tc_fence_after();
-      float2 sum = make_float2(0.f, 0.f);  // finite while every output is
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(kWbScrubbed), it & 1, abort_flag, limit))) { ok = false; break; }
+      const bool odd = *scrubbed != 0;
       const float2 inv2 = make_float2(inv, inv);
       // this row in the store's box (128-byte swizzle: 16-byte chunk k of row r at k ^ (r % 8))
       const int ro = a.o_seq_inner ? gh * a.T + tl : r;
@@ -517,15 +556,11 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 f2 = fmul2(make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2);
-            sum = fadd2(sum, f2);
             ow[q >> 1][16 * (q & 1) + e] = pack_bf16x2(f2.x, f2.y);
           }
         }
       }
       write_lse(l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994530942f);
-      // (a NaN in l is a visible score's: the whole row is NaN by right)
-      const bool odd = live && l == l && !(fabsf(sum.x + sum.y) < INFINITY);
-      const uint32_t odd_rows = __ballot_sync(0xffffffffu, odd);
       // 64 dims at a time through the staging buffer, whose stores warp 7 issues
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -538,14 +573,16 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
                          "r"(ow[hf][4 * k]), "r"(ow[hf][4 * k + 1]), "r"(ow[hf][4 * k + 2]), "r"(ow[hf][4 * k + 3])
                          : "memory");
         }
-        for (uint32_t bad = odd_rows; bad != 0; bad &= bad - 1) {
-          const int src = __ffs(bad) - 1, rs = __shfl_sync(0xffffffffu, ro, src);
-          const uint2 y = window_exact_row(a, x.b, x.kvh, __shfl_sync(0xffffffffu, h, src), __shfl_sync(0xffffffffu, t_row, src));
-          __syncwarp();  // over what the row's thread staged
-          if (lane >> 4 == hf)
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(sbase + L::kO + rs * 128 + ((((lane & 15) >> 1) ^ (rs & 7)) << 4) + (lane & 1) * 8),
-                         "r"(y.x), "r"(y.y)
-                         : "memory");
+        if (odd) {
+          __syncwarp();  // every thread's row is staged
+          const __nv_bfloat16* v = a.V + x.b * a.vb + x.kvh * a.vh + 64 * hf + 2 * lane;
+          const int place = live ? ro : -1;
+          for (int i = 0; i < 32; ++i) {
+            const int rs = __shfl_sync(0xffffffffu, place, i), t = __shfl_sync(0xffffffffu, t_row, i);
+            if (rs < 0) continue;
+            window_restore(a, v, static_cast<int>(a.q_off) + t, x.lo, x.p0, x.p1,
+                           sbase + L::kO + rs * 128 + ((((lane >> 2) ^ (rs & 7)) << 4) | ((lane & 3) << 2)));
+          }
         }
         fence_proxy_async_smem();
         warp_arrive(kWbStoreFull);

@@ -206,3 +206,68 @@ def test_windows_and_sinks_past_32_bits(cuda_ok):
         rbs.swa_prefill(Q, K, V, 4, q_offset=2 ** 64 + 5)
     with pytest.raises(rbs.RbsError, match="2\\^31"):
         rbs.swa_prefill(Q, K, V, 4, q_offset=2 ** 32 + 5)
+
+
+def _with_odd_values(o, see, v):
+    """Outputs [n, D] of finite values, and what they become where visible keys (see [n, keys]) hold the v's that are not."""
+    nan, up, down = (see.astype(np.float32) @ m.astype(np.float32) > 0 for m in (np.isnan(v), np.isposinf(v), np.isneginf(v)))
+    o = np.where(up, np.inf, np.where(down, -np.inf, o))
+    return np.where(nan | (up & down), np.nan, o)
+
+
+@pytest.mark.parametrize("G,Lq,off", [(1, 300, 0), (2, 333, 70), (8, 300, 0), (48, 70, 200), (128, 40, 3)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (7, 3), (1, 1), (40, 0), (64, 16), (100, 17), (150, 70)])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them_alone(cuda_ok, G, Lq, off, window, sinks):
+    """Anywhere, many of them, and in keys that no query sees: the other outputs do not change by a bit."""
+    rng = np.random.default_rng(G + window)
+    n = off + Lq
+    Lk = n + 50  # keys past the last query
+    Q, K, V = _qkv(rng, 1, Lq, 2 * G, 2, Lk)
+    want, wlse = rbs.swa_prefill(Q, K, V, window, sinks, q_offset=off, return_lse=True)
+    see = S.visible(off + np.arange(Lq), np.arange(Lk), window, sinks)
+    values = np.array([np.nan, np.inf, -np.inf])
+    few = [(k, int(rng.integers(2)), int(rng.integers(128))) for k in (0, max(0, sinks - 1), sinks, sinks + 5, n // 2, n - 1, n, Lk - 1)]
+    many = [(int(k), h, int(d)) for k in rng.integers(0, Lk, 60) for h in range(2) for d in rng.integers(0, 128, 2)]
+    whole = [(k, 0, 9) for k in range(Lk)]
+    past = [(k, h, d) for k in range(n, Lk) for h in range(2) for d in range(128)]
+    for places in (few, many, whole, past):
+        W = V.clone()
+        k, h, d = (torch.tensor(x, device="cuda") for x in zip(*places))
+        W[0, k, h, d] = torch.from_numpy(rng.choice(values, len(places))).to(torch.bfloat16).cuda()
+        o, lse = rbs.swa_prefill(Q, K, W, window, sinks, q_offset=off, return_lse=True)
+        assert torch.equal(lse, wlse)
+        for h in range(2 * G):
+            assert np.array_equal(f64(o)[0, :, h], _with_odd_values(f64(want)[0, :, h], see, f64(W)[0, :, h // G]), equal_nan=True)
+    assert rbs.rbs_get_device_error() == 0
+
+
+def _time(f):
+    took = []
+    for i in range(8):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        took.append(a.elapsed_time(b))
+    return sorted(took[3:])[2]
+
+
+def test_a_value_that_every_row_of_a_very_long_prompt_sees_costs_nothing(cuda_ok):
+    """A NaN and an infinity among the first keys of 131,072 tokens, and a dim of infinities alone: rows that see them are
+    not finite there, every other output is what it was, in about the same time."""
+    rng = np.random.default_rng(48)
+    Q, K, V = _qkv(rng, 1, 131072, 4, 1)
+    want, wlse = rbs.swa_prefill(Q, K, V, 0, return_lse=True)
+    clean = _time(lambda: rbs.swa_prefill(Q, K, V, 0))
+    V[0, 0, 0, 3] = float("nan")
+    V[0, 5, 0, 7] = float("inf")
+    V[..., 9] = float("-inf")
+    o, lse = rbs.swa_prefill(Q, K, V, 0, return_lse=True)
+    odd = _time(lambda: rbs.swa_prefill(Q, K, V, 0))
+    assert rbs.rbs_get_device_error() == 0
+    assert torch.isnan(o[..., 3]).all() and torch.isposinf(o[:, 5:, :, 7]).all() and torch.isneginf(o[..., 9]).all()
+    o[..., [3, 9]] = want[..., [3, 9]]
+    o[:, 5:, :, 7] = want[:, 5:, :, 7]
+    assert torch.equal(o, want) and torch.equal(lse, wlse)
+    assert odd < 1.5 * clean, (odd, clean)
