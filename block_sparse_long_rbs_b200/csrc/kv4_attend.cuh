@@ -48,6 +48,7 @@
 // sub-block for 437).
 #pragma once
 
+#include <cfloat>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -77,7 +78,8 @@ struct Kv4AttArgs {
   __nv_bfloat16* o;
   int64_t ob, os, oh;
   float* lse;  // [B, Hq, Lq] or null
-  float scale_log2;  // softmax scale * log2(e) * k_scale
+  float scale_log2;  // softmax scale * log2(e)
+  int k_exp;         // k_scale's power of two
   float v_scale;
   int tiles;  // row tiles of 8 NT rows per (request, KV head)
   float *part_o, *part_ml;  // workspace: two slots per CTA
@@ -200,10 +202,10 @@ template <int NT>
 struct AttSmem {
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kAttWarps * kAttStages * kSubBytes;  // Q fragments [8 groups][NT][32 lanes][8 B]
-  static constexpr int kQExp = kQ + 8 * NT * 256;                        // float [8 NT]: the rows' powers of two
+  static constexpr int kQFac = kQ + 8 * NT * 256;                        // float [8 NT]: what brings the rows' products to exponents
   // a warp's part for joining, float [8 rows][128 + 4], lies over its own ring
   static_assert(kAttStages * kSubBytes >= 8 * 132 * 4, "the ring holds it");
-  static constexpr int kPos = kQExp + 8 * NT * 4;                        // int [8 NT]: the rows' positions, -1: it sees nothing
+  static constexpr int kPos = kQFac + 8 * NT * 4;                        // int [8 NT]: the rows' positions, -1: it sees nothing
   static constexpr int kML = kPos + 8 * NT * 4;                          // float [8 warps][8 NT][2]
   static constexpr int kSums = kML + kAttWarps * 8 * NT * 8;             // int64 [warps]
   static constexpr int kPrefix = kSums + kAttWarps * 8;                  // int32 [B + 1]
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
   constexpr int R = 8 * NT;  // rows of a tile
   extern __shared__ __align__(16) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
-  float* qexp = reinterpret_cast<float*>(smem + L::kQExp);
+  float* qfac = reinterpret_cast<float*>(smem + L::kQFac);
   int* qpos = reinterpret_cast<int*>(smem + L::kPos);
   float* ml = reinterpret_cast<float*>(smem + L::kML);
   int64_t* sums = reinterpret_cast<int64_t*>(smem + L::kSums);
@@ -319,7 +321,13 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + ((k0 & 7) >> 1) * 8 + (k0 >> 3) * 4), "r"(w0) : "memory");
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (((k0 + 2) & 7) >> 1) * 8 + (k0 >> 3) * 4), "r"(w1) : "memory");
       if (lane == 0) {
-        qexp[n] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        // scale_log2 k_scale 2^e, the powers of two in halves that fp32 holds.  A factor outside fp32's
+        // range comes from a row whose scores are all negligible (products stay below 2^31), or whose
+        // scores fp32 does not hold: the end of the range serves, where 0 or an infinity would make a
+        // masked score's -inf, or a product of 0, a NaN.
+        const int f = e + a.k_exp, half = f >> 1;
+        const float fac = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + half) << 23) * __uint_as_float(static_cast<uint32_t>(127 + f - half) << 23);
+        qfac[n] = fminf(fmaxf(fac, FLT_MIN), FLT_MAX);
         const int p = row < rows ? rg.first_q + row / a.G : -1;
         qpos[n] = p < rg.len ? p : -1;
       }
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        sc[nt][i] = a.scale_log2 * qexp[8 * nt + 2 * j + i];
+        sc[nt][i] = qfac[8 * nt + 2 * j + i];
         m_run[nt][i] = kAttNoMax;
         l_run[nt][i] = 0.f;
       }

@@ -1481,7 +1481,8 @@ rbs_status kv4_attend(const rbs_bf16_tensor* Q, const rbs_kv4_cache* cache, cons
   a.ob = O->stride_b; a.os = O->stride_s; a.oh = O->stride_h;
   a.lse = lse;
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(RBS_HEAD_DIM));
-  a.scale_log2 = scale * 1.4426950408889634f * cache->k_scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.k_exp = std::ilogb(cache->k_scale);
   a.v_scale = cache->v_scale;
   a.tiles = static_cast<int>(tiles);
   a.ctas = std::min(attend_ctas(di, nt), kAttMaxCtas);

@@ -452,3 +452,15 @@ def test_integers_past_32_bits_are_refused(cuda_ok):
             rbs.kv4_load(rbs.KV4Cache(cache.data, bad), n[None])
         with pytest.raises(ValueError, match="rope_style"):
             rbs.rope_qk_norm(K, K, None, None, ints(np.arange(4)), 1e4, rope_style=bad)
+
+
+@pytest.mark.parametrize("qs,gk,scale", [(1e-30, 2.0 ** -64, None), (1.0, 2.0 ** -64, 1e-44), (1e-37, 2.0 ** 64, 2e19)])
+def test_attend_factors_of_the_scores_beyond_fp32(cuda_ok, qs, gk, scale):
+    """softmax_scale, k_scale and the size of a query row, whose product leaves fp32's range while the scores do not: rows
+    of equal weights, and ordinary ones."""
+    rng = np.random.default_rng(64)
+    held = Held(rng, [40, 7, 200], 1, 32, gk=gk, k_scale=gk)
+    Q = randn(rng, 3, 2, 4, 128, scale=qs)
+    for kw in ({}, dict(window=9, sinks=3)):
+        o, lse = _attend(held, Q, softmax_scale=scale, **kw)
+        _check(o, lse, held, Q, scale=scale, **kw)
