@@ -60,7 +60,7 @@ constexpr int kAttThreads = kAttWarps * 32;
 constexpr int kAttStages = 5;
 constexpr int kAttMaxBatch = 4096;
 constexpr float kAttPShift = 6.f;  // P carries 2^6
-constexpr float kAttNoMax = -1e30f;  // the running maximum of a row that has seen no key
+constexpr float kAttNoMax = -FLT_MAX;  // the running maximum of a row that has seen no key: below every score, and finite
 
 struct Kv4AttArgs {
   const uint8_t* data;
@@ -409,18 +409,29 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
             if (!see) c[nt][q] = -INFINITY;
           }
       }
-      // exponents of P; the running maximum moves only when a score passes it by 2^8
+      // exponents of P; the running maximum moves only when a score passes it by 2^8.  The scaled scores are
+      // rounded before the maximum is taken off, as the maximum itself was: one rounding for both would leave the
+      // difference of a rounded and an exact product, which past 2^28 is more than fp16's exponents hold
+      // (in pairs this takes no more instructions).
+      auto exponents = [&](int nt, int i) {  // of keys r (i = 0) or r + 8 (i = 2)
+        return fadd2(fmul2(make_float2(c[nt][i], c[nt][i + 1]), make_float2(sc[nt][0], sc[nt][1])),
+                     make_float2(kAttPShift - m_run[nt][0], kAttPShift - m_run[nt][1]));
+      };
       float e[NT][4];
       bool up = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) e[nt][q] = fmaf(c[nt][q], sc[nt][q & 1], kAttPShift - m_run[nt][q & 1]);
+        for (int q = 0; q < 4; q += 2) {
+          const float2 x = exponents(nt, q);
+          e[nt][q] = x.x;
+          e[nt][q + 1] = x.y;
+        }
         up = up || fmaxf(fmax3(e[nt][0], e[nt][1], e[nt][2]), e[nt][3]) > 8.f + kAttPShift;
       }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float mx = fmaxf(c[nt][i], c[nt][2 + i]);
@@ -436,9 +447,14 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
               o[s][nt][i] *= f;
               o[s][nt][2 + i] *= f;
             }
-            e[nt][i] = fmaf(c[nt][i], sc[nt][i], kAttPShift - mn);
-            e[nt][2 + i] = fmaf(c[nt][2 + i], sc[nt][i], kAttPShift - mn);
           }
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
+            const float2 x = exponents(nt, q);
+            e[nt][q] = x.x;
+            e[nt][q + 1] = x.y;
+          }
+        }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {

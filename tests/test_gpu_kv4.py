@@ -464,3 +464,33 @@ def test_attend_factors_of_the_scores_beyond_fp32(cuda_ok, qs, gk, scale):
     for kw in ({}, dict(window=9, sinks=3)):
         o, lse = _attend(held, Q, softmax_scale=scale, **kw)
         _check(o, lse, held, Q, scale=scale, **kw)
+
+
+@pytest.mark.parametrize("lens", [[60], [3000, 50]])
+def test_attend_scores_far_below_zero(cuda_ok, lens):
+    """Every score of a row below -1e34: the largest one takes the whole weight all the same."""
+    rng = np.random.default_rng(65)
+    held = Held(rng, lens, 1, 32)
+    B, n = held.slots.shape
+    K = torch.full((B, n, 1, 128), -2.0, dtype=torch.bfloat16, device="cuda")
+    K[:, 17] = -1.0
+    K[:, 18:] = -6.0
+    rbs.kv4_append(held.cache, K, randn(rng, B, n, 1, 128), ints(held.slots))
+    k, v = rbs.kv4_load(held.cache, ints(held.slots))
+    o, lse = _attend(held, torch.full((B, 1, 2, 128), 1e33, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(o, v[:, 17:18].expand(B, 1, 2, 128))
+    # (the cache holds -1 as code 6 times the scale e4m3(1 / 6) = 11 / 64: -1.03125)
+    want = f64(k)[:, 17].sum() / B * float(torch.tensor(1e33, dtype=torch.bfloat16)) / 128 ** 0.5
+    assert (np.abs(f64(lse) / want - 1) < 2.0 ** -20).all()  # a handful of fp32 roundings
+
+
+@pytest.mark.parametrize("size", [1e4, 1e5, 1e7])
+@pytest.mark.parametrize("Lq", [1, 2])
+def test_attend_scores_far_apart(cuda_ok, size, Lq):
+    """Queries and keys whose scores are far past 2^28: each row is the value of its highest key."""
+    rng = np.random.default_rng(68)
+    held = Held(rng, [500, 3000, 40], 2, 32, gk=2.0 ** 12, k_scale=size)
+    Q = randn(rng, 3, Lq, 6, 128, scale=size)
+    o, lse = _attend(held, Q)
+    _check(o, lse, held, Q)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
