@@ -351,14 +351,17 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int q = 0; q < 4; ++q) o[s][nt][q] = 0.f;
-    // positions of the tile's queries: [p_lo, p_hi], and whether all of them exist
+    // positions of the tile's live queries: [p_lo, p_hi].  Rows of a padded batch that are past the request's tokens or
+    // before its first take part in sub-blocks that the live rows see whole, whatever comes out: they are emptied when
+    // the warps join (three live tokens of four over 65,536: 101 us a call against 288 when one such row made every
+    // sub-block a partly visible one; four live ones 100).
     const int t_lo = row0 / a.G, t_hi = (min(row0 + R, rows) - 1) / a.G;
-    const int p_lo = rg.first_q + t_lo, p_hi = rg.first_q + t_hi;
-    const bool all_live = p_lo >= 0 && p_hi < rg.len;
-    // sub-blocks that every row sees whole: below full_sink, and in [full_lo, full_hi)
-    const int full_hi = all_live ? ((p_lo + 1) >> 4) - shift : 0;
+    const int p_lo = max(rg.first_q + t_lo, 0);
+    const int p_hi = max(0, static_cast<int>(min(static_cast<int64_t>(rg.first_q) + t_hi, static_cast<int64_t>(rg.len) - 1)));
+    // sub-blocks that every live row sees whole: below full_sink, and in [full_lo, full_hi)
+    const int full_hi = ((p_lo + 1) >> 4) - shift;
     const int full_lo = a.window == 0 ? 0 : static_cast<int>((static_cast<uint32_t>(max(p_hi - a.window + 1, 0)) + 15u) >> 4) - shift;
-    const int full_sink = all_live ? min(rg.sink, a.sinks >> 4) : 0;
+    const int full_sink = min(rg.sink, a.sinks >> 4);
 
     // ---- the sub-blocks: products of one, then scores of the next
     uint32_t p0[NT], p1[NT];  // P^T, the second product's operand: keys 2j, 2j + 1 (+ 8) of row r
@@ -614,6 +617,11 @@ __global__ void __launch_bounds__(kAttThreads, NT <= 2 ? 2 : 1) kv4_attend_kerne
         acc.w = fmaf(f, x.w, acc.w);
       }
       if (row < rows) {
+        if (qpos[n] < 0) {  // a row that sees nothing
+          m = kAttNoMax;
+          l = 0.f;
+          acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         if (whole) {
           const float inv = l == 0.f ? 0.f : a.v_scale / l;  // a NaN stays one
           const int t = row / a.G, h = kvh * a.G + row - t * a.G;

@@ -494,3 +494,45 @@ def test_attend_scores_far_apart(cuda_ok, size, Lq):
     o, lse = _attend(held, Q)
     _check(o, lse, held, Q)
     assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("lens,G,Lq", [([700, 90, 16, 5], 2, 4), ([5000, 3], 8, 4), ([2000, 40], 6, 20)])
+def test_attend_padded_rows_that_hold_anything(cuda_ok, lens, G, Lq):
+    """Rows of a padded batch past a request's tokens or before its first: empty, whatever their queries hold, and the
+    rows beside them are what they are alone."""
+    rng = np.random.default_rng(66)
+    held = Held(rng, lens, 2, 32)
+    Q = randn(rng, len(lens), Lq, 2 * G, 128)
+    for back in (1, Lq - 1, -2):  # live rows at the front, or two dead ones there
+        starts = held.lens - back if back > 0 else np.full(len(lens), -2)
+        p = starts[:, None] + np.arange(Lq)
+        dead = (p < 0) | (p >= held.lens[:, None])
+        odd = Q.clone()
+        odd[torch.from_numpy(dead).cuda()] = float("nan")
+        for kw in ({}, dict(window=40, sinks=21)):
+            o, lse = _attend(held, odd, starts=starts, **kw)
+            _check(o, lse, held, Q, starts=starts, **kw)
+
+
+def test_attend_padded_rows_cost_what_full_rows_do(cuda_ok):
+    """Three of four drafted tokens live, over long caches: the sub-blocks that every live row sees whole take one pass.
+    (Measured ratio of the times 1.0; four passes over each sub-block made it 2 and more.)"""
+    rng = np.random.default_rng(67)
+    n, page, B = 65536, 64, 4
+    data = torch.zeros(B * n // page, 4, rbs.rbs_kv4_page_bytes(page), dtype=torch.uint8, device="cuda")
+    cache, table = rbs.KV4Cache(data, page), ints(np.arange(B * n // page).reshape(B, -1))
+    Q, lens = randn(rng, B, 4, 32, 128), ints([n] * B)
+    took = []
+    for live in (4, 3):
+        starts, times = ints([n - live] * B), []
+        for i in range(13):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(10):
+                rbs.kv4_attend(Q, cache, table, lens, starts=starts)
+            b.record()
+            b.synchronize()
+            if i >= 3:
+                times.append(a.elapsed_time(b))
+        took.append(sorted(times)[5])
+    assert took[1] < 1.5 * took[0], took
