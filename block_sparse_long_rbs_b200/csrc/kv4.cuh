@@ -126,11 +126,11 @@ __global__ void __launch_bounds__(kExtThreads) kv4_extend_kernel(const __grid_co
     const int64_t f = head + first[b - b0];
     int32_t* row = a.table + b * a.table_b;
     for (int e = had + blockIdx.y * kExtThreads + threadIdx.x; e < has; e += stride) row[e] = free_page(f + e - had);
-    for (int i = blockIdx.y * kExtThreads + threadIdx.x; i < a.max_new; i += stride) {
-      const int p = old_len + i;
+    // (64 bits: a step past a max_new near 2^31 would come out negative, and write there)
+    for (int64_t i = blockIdx.y * kExtThreads + threadIdx.x; i < a.max_new; i += stride) {
       int32_t slot = -1, pos = -1;
       if (i < new_len - old_len) {
-        const int e = p / a.page;
+        const int p = old_len + static_cast<int>(i), e = p / a.page;
         const int32_t pg = e < had ? row[e] : free_page(f + e - had);
         pos = p;
         // (an entry that is no page of any cache gives no slot)

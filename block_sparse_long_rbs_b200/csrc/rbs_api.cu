@@ -1392,7 +1392,7 @@ rbs_status kv4_extend(int32_t* block_table, int64_t table_stride, int32_t batch,
   const int want = 2 * di->sms;
   const int per_cta = std::min(kExtThreads, std::max(1, (batch + want - 1) / want));
   const int gx = (batch + per_cta - 1) / per_cta;
-  const int gy = std::max(1, std::min({want / gx, (max_new + kExtThreads - 1) / kExtThreads, 65535}));
+  const int gy = std::max(1, std::min({want / gx, (max_new - 1) / kExtThreads + 1, 65535}));
   kv4_extend_kernel<<<dim3(gx, gy), kExtThreads, 0, stream>>>(a, per_cta);
   return check_launch("kv4_extend_kernel");
 }

@@ -536,3 +536,18 @@ def test_attend_padded_rows_cost_what_full_rows_do(cuda_ok):
                 times.append(a.elapsed_time(b))
         took.append(sorted(times)[5])
     assert took[1] < 1.5 * took[0], took
+
+
+def test_extend_as_many_new_tokens_as_int32_holds(cuda_ok):
+    """max_new = 2^31 - 1: every slot and position of the row is written, and nothing beside them."""
+    n = 2 ** 31 - 1
+    hold = [torch.full((n + 4096,), 77, dtype=torch.int32, device="cuda") for _ in range(2)]
+    slots, pos = (x[2048:2048 + n].view(1, n) for x in hold)
+    table = ints([[-1, -1, -1]])
+    assert rbs.rbs_get_device_error() == 0
+    rbs.kv4_extend(table, ints([0]), ints([40]), ints([7, 3, 5, 9]), ints([1]), n, 16, slots=slots, pos=pos)
+    assert rbs.rbs_get_device_error() == 0 and table.tolist() == [[3, 5, 9]]
+    assert pos[0, :40].tolist() == list(range(40)) and slots[0, :40].tolist() == [(3, 5, 9)[t // 16] * 16 + t % 16 for t in range(40)]
+    for x in hold:
+        assert (x[:2048] == 77).all() and (x[2048 + n:] == 77).all()
+        assert x[2088:2048 + n].amax() == -1 and x[2088:2048 + n].amin() == -1
