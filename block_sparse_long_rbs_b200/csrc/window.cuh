@@ -18,7 +18,9 @@
 //              scores, masks them in tiles that some row sees only in part,
 //              takes the maximum (the running maximum moves, and O is rescaled,
 //              only when it grows by more than 2^8), writes
-//              P = exp2(S c - m) as bf16 pairs over the scores, and at the end
+//              P = exp2(S c - m) as bf16 pairs over the scores (2^-8 relative:
+//              V is bf16 and both operands of a product have one type; V's
+//              range does not fit fp16), and at the end
 //              stages O / l for a TMA store and writes the LSE.
 //   warp 4     Q and K producer, warp 5 V producer (TMA, one lane)
 //   warp 6     TMEM allocator, issuer of S = Q K^T (both operands in shared memory)
@@ -48,8 +50,8 @@
 // Masked scores are replaced before the softmax, so NaN keys stay out.  A masked
 // value still meets its zero weight in the product, and zero times a NaN or an
 // infinity is NaN.  The keys that some row of an item does not see are few: the
-// window's edges (fewer than T keys each) and what the last tile holds past the
-// last token (the copies fill what lies past the sinks with zeros).  Warp 7
+// window's edges (fewer than T keys each) and what the last step of 16 keys holds
+// past the last token (the copies fill what lies past the sinks with zeros).  Warp 7
 // looks through those before their product and sets what is not finite there to
 // zero; where it found some, each row adds those that it does see (whatever
 // their weights, they make the sum non-finite) to its outputs at the end.  What
@@ -115,8 +117,7 @@ enum : int {
   kWbOEmpty = kWbOFull + 1,
   kWbStoreFull = kWbOEmpty + 1,  // 64 dims of the outputs are staged
   kWbStoreEmpty = kWbStoreFull + 1,
-  kWbScrubbed = kWbStoreEmpty + 1,  // every tile of the item has been looked through
-  kWbDrain = kWbScrubbed + 1,    // + issuer
+  kWbDrain = kWbStoreEmpty + 1,  // + issuer
   kWbNum = kWbDrain + 2
 };
 static_assert(kWbNum * 8 + 16 <= 256, "barrier area");
@@ -170,64 +171,76 @@ __device__ __forceinline__ int win_key0(const WinItem& x, int t) {
   return x.lo - (x.merged ? kWinSinkRows : 0) + (t - x.n_sink) * kWinKeys;
 }
 
-// Bit patterns of bf16 pairs that hold a NaN or an infinity.
-__device__ __forceinline__ bool bf16x2_odd(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-
-// Columns [c0, c1) of a value tile in shared memory, by a whole warp: what is not finite becomes zero.
-__device__ __forceinline__ bool window_scrub(uint32_t tile, int c0, int c1) {
+// Columns [c0, c1) of a value tile in shared memory, by a whole warp: stays
+// zero (of either sign) while all of them are finite, since 0 times a value
+// that is not is NaN.
+__device__ __forceinline__ void window_look(uint32_t tile, int c0, int c1, uint32_t& acc) {
   const int lane = threadIdx.x & 31;
-  bool found = false;
 #pragma unroll 2
   for (int c = c0 + (lane >> 3); c < c1; c += 4) {
+    const uint32_t at = tile + c * 128 + (lane & 7) * 16;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const uint32_t at = tile + hf * (kWinKeys * 128) + c * 128 + (lane & 7) * 16;
       uint32_t w[4];
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
-      uint32_t top = 0;  // the largest size of each half, by its bits
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at + hf * (kWinKeys * 128)) : "memory");
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
-      if (bf16x2_odd(top)) {
-        found = true;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
-          if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu;
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-      }
+      for (int k = 0; k < 4; ++k) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[k]), "r"(0u));
     }
   }
-  return __any_sync(0xffffffffu, found);
 }
 
-// What window_scrub took from the query at position p, back onto 64 dims of its
-// staged outputs, by a whole warp, two dims a lane: v points at the lane's
-// dims of key 0, out at its place in the staged row.
-__device__ __noinline__ void window_restore(const WinArgs& a, const __nv_bfloat16* v, int p, int lo, int p0, int p1, uint32_t out) {
-  float2 add = make_float2(0.f, 0.f);  // of values that are not finite alone
-  auto take = [&](int s0, int s1) {    // keys s0 .. s1
-#pragma unroll 4
-    for (int s = s0; s <= s1; ++s) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(v + s * a.vs));
-      if ((w & 0x7f80u) == 0x7f80u) add.x += bf16lo(w);
-      if ((w & 0x7f800000u) == 0x7f800000u) add.y += bf16hi(w);
+// What is not finite in those columns becomes zero.
+__device__ __noinline__ void window_scrub(uint32_t tile, int c0, int c1) {
+  const int lane = threadIdx.x & 31;
+  for (int c = c0 + (lane >> 3); c < c1; c += 4)
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t at = tile + (k >> 2) * (kWinKeys * 128) + c * 128 + (lane & 7) * 16 + (k & 3) * 4;
+      uint32_t w;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+      if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+      if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
     }
-  };
-  // the keys of either edge that the row sees: in its window, then its sinks
-  // among them (a key taken twice changes nothing)
-  const int see = p - a.W + 1, lo_end = min(min(p1 - a.W, p), a.Lk - 1), hi_from = max(lo, p0 + 1), hi_end = min(p, a.Lk - 1);
-  take(max(lo, see), lo_end);
-  take(lo, min(a.S - 1, lo_end));
-  take(max(hi_from, see), hi_end);
-  take(hi_from, min(a.S - 1, hi_end));
-  uint32_t o;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(o) : "r"(out) : "memory");
-  if (add.x != 0.f) o = (o & 0xffff0000u) | (pack_bf16x2(bf16lo(o) + add.x, 0.f) & 0xffffu);
-  if (add.y != 0.f) o = (o & 0xffffu) | (pack_bf16x2(0.f, bf16hi(o) + add.y) & 0xffff0000u);
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(out), "r"(o) : "memory");
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// What window_scrub took from the queries of a warp's 32 rows, back onto half
+// hf (64 dims) of their outputs staged at `stage`, a row after the other, two
+// dims a lane.  row: this thread's row in the staging buffer, -1 for none;
+// t: its token.  Only items whose values window_scrub changed come here; they
+// are formed anew from w, to keep the registers of the others.
+__device__ __noinline__ void window_restore(const WinArgs& a, int w, int hf, int row, int t, uint32_t stage) {
+  const int lane = threadIdx.x & 31;
+  const WinItem x = win_item(a, w);
+  const __nv_bfloat16* v = a.V + x.b * a.vb + x.kvh * a.vh + 64 * hf + 2 * lane;
+  __syncwarp();  // every thread's row is staged
+  for (int i = 0; i < 32; ++i) {
+    const int r = __shfl_sync(0xffffffffu, row, i), p = static_cast<int>(a.q_off) + __shfl_sync(0xffffffffu, t, i);
+    if (r < 0) continue;
+    float2 add = make_float2(0.f, 0.f);  // of values that are not finite alone
+    auto take = [&](int s0, int s1) {    // keys s0 .. s1
+#pragma unroll 4
+      for (int s = s0; s <= s1; ++s) {
+        const uint32_t y = __ldg(reinterpret_cast<const uint32_t*>(v + s * a.vs));
+        if ((y & 0x7f80u) == 0x7f80u) add.x += bf16lo(y);
+        if ((y & 0x7f800000u) == 0x7f800000u) add.y += bf16hi(y);
+      }
+    };
+    // the keys of either edge that the row sees: in its window, then its sinks
+    // among them (a key taken twice changes nothing)
+    const int see = p - a.W + 1, end = min(p, a.Lk - 1), lo_end = min(x.p1 - a.W, end), hi_from = max(x.lo, x.p0 + 1);
+    take(max(x.lo, see), lo_end);
+    take(x.lo, min(a.S - 1, lo_end));
+    take(max(hi_from, see), end);
+    take(hi_from, min(a.S - 1, end));
+    const uint32_t out = stage + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2));
+    uint32_t o;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(o) : "r"(out) : "memory");
+    if (add.x != 0.f) o = (o & 0xffff0000u) | (pack_bf16x2(bf16lo(o) + add.x, 0.f) & 0xffffu);
+    if (add.y != 0.f) o = (o & 0xffffu) | (pack_bf16x2(0.f, bf16hi(o) + add.y) & 0xffff0000u);
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(out), "r"(o) : "memory");
+  }
 }
 
 __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __grid_constant__ WinArgs a) {
@@ -259,11 +272,10 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
       mbar_init(bar(kWbPFull + s), 4);
     }
     for (int s = 0; s < 4; ++s) mbar_init(bar(kWbPVDone + s), 1);
-    mbar_init(bar(kWbOFull), 1);
+    mbar_init(bar(kWbOFull), 2);  // the products, and the word on what was taken out of the values
     mbar_init(bar(kWbOEmpty), 4);
     mbar_init(bar(kWbStoreFull), 4);
     mbar_init(bar(kWbStoreEmpty), 1);
-    mbar_init(bar(kWbScrubbed), 1);
     mbar_init(bar(kWbDrain), 1);
     mbar_init(bar(kWbDrain + 1), 1);
     *abort_flag = 0;
@@ -379,19 +391,25 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
           // the tile's keys that some row does not see, while its weights are
           // still being formed: at the window's lower edge, and past the first token
           if (t == 0) odd = false;
+          const int k0 = win_key0(x, t);
+          // steps of 16 keys up to the last one that some row sees
+          const int steps = min(kWinKeys / 16, ((t < x.n_sink ? x.sinks - 1 : min(x.p1, a.Lk - 1)) - k0) / 16 + 1);
           if (t >= x.n_sink) {
-            const int k0 = win_key0(x, t), c0 = t == 0 && x.merged ? kWinSinkRows : 0;
-            const bool lower = window_scrub(sV + s * L::kKVBytes, c0, min(kWinKeys, x.p1 - a.W + 1 - k0));
-            const bool upper = window_scrub(sV + s * L::kKVBytes, max(c0, x.p0 + 1 - k0), min(kWinKeys, a.Lk - k0));
-            if (lower || upper) {
-              fence_proxy_async_smem();
-              __syncwarp();
+            const int c0 = t == 0 && x.merged ? kWinSinkRows : 0;
+            const int lo_end = min(kWinKeys, x.p1 - a.W + 1 - k0), hi_from = max(c0, x.p0 + 1 - k0), hi_end = min(16 * steps, a.Lk - k0);
+            const uint32_t tile = sV + s * L::kKVBytes;
+            uint32_t acc = 0;
+            window_look(tile, c0, lo_end, acc);
+            window_look(tile, hi_from, hi_end, acc);
+            if (__any_sync(0xffffffffu, (acc & 0x7fff7fffu) != 0)) {
+              window_scrub(tile, c0, lo_end);
+              window_scrub(tile, hi_from, hi_end);
               odd = true;
             }
           }
           if (t == x.n - 1 && lane == 0) {
             *scrubbed = odd;
-            mbar_arrive(bar(kWbScrubbed));
+            mbar_arrive(bar(kWbOFull));
           }
           if (!wait(kWbPFull + b, (g >> 1) & 1)) { ok = false; break; }
           if (t == 0 && it > 0 && !wait(kWbOEmpty, (it - 1) & 1)) { ok = false; break; }
@@ -399,7 +417,8 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
           const uint64_t vd = vdesc0 + s * kStageUnits;
 #pragma unroll
           for (int kk = 0; kk < kWinKeys / 16; ++kk)
-            umma_ts_warp(tmem + L::kColO, tmem + L::col_s(b) + kk * 8, vd + kk * (2048 >> 4), idPV, (t == 0 && kk == 0) ? 0u : 1u);
+            if (kk < steps)
+              umma_ts_warp(tmem + L::kColO, tmem + L::col_s(b) + kk * 8, vd + kk * (2048 >> 4), idPV, (t == 0 && kk == 0) ? 0u : 1u);
           umma_commit_warp(bar(kWbPVDone + (g & 3)));
           if (t == x.n - 1) umma_commit_warp(bar(kWbOFull));
         }
@@ -537,7 +556,6 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (!__all_sync(0xffffffffu, mbar_wait(bar(kWbOFull), it & 1, abort_flag, limit))) { ok = false; break; }
       tc_fence_after();
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(kWbScrubbed), it & 1, abort_flag, limit))) { ok = false; break; }
       const bool odd = *scrubbed != 0;
       const float2 inv2 = make_float2(inv, inv);
       // this row in the store's box (128-byte swizzle: 16-byte chunk k of row r at k ^ (r % 8))
@@ -573,17 +591,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) swa_prefill_kernel(const __gri
                          "r"(ow[hf][4 * k]), "r"(ow[hf][4 * k + 1]), "r"(ow[hf][4 * k + 2]), "r"(ow[hf][4 * k + 3])
                          : "memory");
         }
-        if (odd) {
-          __syncwarp();  // every thread's row is staged
-          const __nv_bfloat16* v = a.V + x.b * a.vb + x.kvh * a.vh + 64 * hf + 2 * lane;
-          const int place = live ? ro : -1;
-          for (int i = 0; i < 32; ++i) {
-            const int rs = __shfl_sync(0xffffffffu, place, i), t = __shfl_sync(0xffffffffu, t_row, i);
-            if (rs < 0) continue;
-            window_restore(a, v, static_cast<int>(a.q_off) + t, x.lo, x.p0, x.p1,
-                           sbase + L::kO + rs * 128 + ((((lane >> 2) ^ (rs & 7)) << 4) | ((lane & 3) << 2)));
-          }
-        }
+        if (odd) window_restore(a, w, hf, live ? ro : -1, t_row, sbase + L::kO);
         fence_proxy_async_smem();
         warp_arrive(kWbStoreFull);
       }
