@@ -215,10 +215,11 @@ __device__ __noinline__ void window_restore(const WinArgs& a, int w, int hf, int
   const WinItem x = win_item(a, w);
   const __nv_bfloat16* v = a.V + x.b * a.vb + x.kvh * a.vh + 64 * hf + 2 * lane;
   __syncwarp();  // every thread's row is staged
+  float2 add = make_float2(0.f, 0.f);  // of values that are not finite alone
+  int token = -1;                      // whose they are: the rows of a token's heads share them
   for (int i = 0; i < 32; ++i) {
     const int r = __shfl_sync(0xffffffffu, row, i), p = static_cast<int>(a.q_off) + __shfl_sync(0xffffffffu, t, i);
     if (r < 0) continue;
-    float2 add = make_float2(0.f, 0.f);  // of values that are not finite alone
     auto take = [&](int s0, int s1) {    // keys s0 .. s1
 #pragma unroll 4
       for (int s = s0; s <= s1; ++s) {
@@ -229,11 +230,15 @@ __device__ __noinline__ void window_restore(const WinArgs& a, int w, int hf, int
     };
     // the keys of either edge that the row sees: in its window, then its sinks
     // among them (a key taken twice changes nothing)
-    const int see = p - a.W + 1, end = min(p, a.Lk - 1), lo_end = min(x.p1 - a.W, end), hi_from = max(x.lo, x.p0 + 1);
-    take(max(x.lo, see), lo_end);
-    take(x.lo, min(a.S - 1, lo_end));
-    take(max(hi_from, see), end);
-    take(hi_from, min(a.S - 1, end));
+    if (p != token) {
+      token = p;
+      add = make_float2(0.f, 0.f);
+      const int see = p - a.W + 1, end = min(p, a.Lk - 1), lo_end = min(x.p1 - a.W, end), hi_from = max(x.lo, x.p0 + 1);
+      take(max(x.lo, see), lo_end);
+      take(x.lo, min(a.S - 1, lo_end));
+      take(max(hi_from, see), end);
+      take(hi_from, min(a.S - 1, end));
+    }
     const uint32_t out = stage + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2));
     uint32_t o;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(o) : "r"(out) : "memory");
