@@ -2,8 +2,8 @@
 // attention, the 4-bit cache) without the interpreter: a decoding step makes
 // several of them per layer, and reading a tensor's attributes, allocating the
 // outputs and building the C structures in Python took most of a call (norm
-// and rotation of 64 tokens: 15 us a call in Python, 9 us here, of which 3 us
-// on the GPU; the cache's paging 16 and 5.5 us).
+// and rotation of 64 tokens: 15 us a call in Python, 7 us here, of which 3 us
+// on the GPU; the cache's paging 16 and 6 us).
 //
 // Each function takes the Python call's arguments, and
 //   - returns None, having done nothing, when an argument is not plainly what

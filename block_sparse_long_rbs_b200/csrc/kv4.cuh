@@ -80,8 +80,8 @@ __device__ __forceinline__ void extend_pages(const ExtendArgs& a, int b, int& ol
   has = (new_len + a.page - 1) / a.page;
 }
 
-// Bound by the launch: 64 requests and one token each 2.7 us, 4,096 tokens each
-// 3.9 us.
+// Bound by the launch: 64 requests and one token each 3.0 us, 4,096 tokens each
+// 4.5 us.
 // CTAs split requests' output rows (blockIdx.y: slices of one request's slots
 // and pages).  Each sums the page counts of the requests before its own from
 // the lengths; the entries a CTA writes to the table are never read by another
@@ -253,9 +253,8 @@ __device__ __forceinline__ void transpose8(uint32_t& lo, uint32_t& hi, int lane,
 // row, which move their bytes to the layout's order among themselves: a thread
 // writes (reads) eight bytes of the row's key codes and eight of its value
 // codes.  512 + 144 bytes per row have to move; measured: 16,384 tokens of 4 KV
-// heads written and read back in 22.4 us (13.3 at a copy's rate), bound by
-// instruction issue (69% of the slots in the writer); 64 tokens in 5.1 us, two
-// launches.
+// heads written and read back in 23.3 us (13.3 at a copy's rate), the writer with
+// 69% of the issue slots taken; 64 tokens in 5.9 us, two launches.
 __global__ void __launch_bounds__(kIoThreads) kv4_append_kernel(const __grid_constant__ Kv4IoArgs a) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kIoThreads / 8) + (threadIdx.x >> 3);
   const int s = threadIdx.x & 7;

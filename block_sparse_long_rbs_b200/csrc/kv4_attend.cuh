@@ -22,7 +22,7 @@
 // become fp16 by the e2m1 conversion, and times their scale stay exact; Q is
 // brought to fp16 by a power of two per row (bf16's 8 bits fit fp16's 11; values
 // more than 2^26 below the row's largest lose bits that fp32 sums would lose as
-// well); P = 2^6 exp2(s - m) is rounded to fp16 once (2^-12 relative), m at most
+// well); P = 2^6 exp2(s - m) is rounded to fp16 once (2^-11 relative), m at most
 // 2^8 below the running maximum, so that an update is rare; keys down to 2^-31
 // of the largest still count.  Sums and outputs stay in fp32.
 // Keys that no row may see get the value scale 0 (their bytes may be
@@ -31,12 +31,16 @@
 // may not see set to zero.
 // 144 bytes per cached token and KV head have to be read.  Measured: 64 requests of
 // 8,192 to 16,384 tokens, 32 q / 4 KV heads (about 456 MB): 118 us, 3.9 TB/s of the
-// 6.46 a copy reaches; bound by instruction issue (60% of the slots, about 400 warp
+// 6.46 a copy reaches; most of the time goes to instruction issue (61% of the slots, about 400 warp
 // instructions per sub-block, of them 88 conversions, 64 scalings, 16 matrix
-// instructions) with four warps per scheduler.  32 rows per tile: the outputs
+// instructions), the rest to latencies that four warps per scheduler leave open.
+// 32 rows per tile: the outputs
 // take 128 registers of every thread, one CTA per SM and two warps per
 // scheduler are left, and latency bounds it (four drafted tokens of four requests
-// of up to 131,072 tokens: 122 us).  Measured and left: tiles of 16 rows
+// of 65,536 to 131,072 tokens: 131 us for 383,000 tokens in all, 139 for 406,000).
+// Spilled registers: 24 bytes of stores there, 64 for 16 rows of one token, 196
+// for 16 rows of several, where two CTAs per SM allow 128 registers (what they
+// cost apart has not been measured); none for 8 rows.  Measured and left: tiles of 16 rows
 // there, reading the cache twice (226 against 165 us); pairs of warps that share
 // a sub-block's rows and dims (178 against 133 us: keys converted twice); rings of
 // 4 and 6 stages (120 and 118 us for the 64 requests); two chains of products

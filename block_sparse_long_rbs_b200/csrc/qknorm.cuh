@@ -10,7 +10,7 @@
 // (t - rint(t), exact); only the remainder in [-1/2, 1/2] is rounded to fp32
 // and goes to the approximate sine and cosine, whose absolute error on
 // [-pi, pi] is below 2^-20.5: with the angle's own rounding an output is off by
-// less than 2^-19 of its pair's size before its rounding to bf16 (2^-9).
+// less than 2^-19 of its pair's size before its rounding to bf16 (2^-8).
 // f_m = f_base r^step with eight bases and eight powers, so a thread forms its
 // eight frequencies with eight products.
 //
@@ -24,7 +24,8 @@
 // r (C lo + D hi), two pairs at a time in packed fp32; the loads of four heads
 // are issued together.
 // Bound by memory: 512 bytes per head row (16,384 tokens of 32 + 4 heads: 53 us,
-// 5.7 TB/s of the 6.46 a copy reaches; 64 tokens: 2.8 us, the launch).
+// 5.7 TB/s of the 6.46 a copy reaches, with 44 and 52 bytes of spilled registers
+// in the two styles; 64 tokens: 3.1 us, the launch).
 #pragma once
 
 #include "common.cuh"

@@ -28,20 +28,22 @@
 //              and of the outputs' stores
 // TMEM columns: S buffers [0, 64) and [64, 128), O [128, 256).
 //
-// Bound by the softmax warps: per 64 scores of two rows a scheduler has 1024
-// cycles of exponentials (16 a clock and SM), and the two warps that share it
-// overlap them with only part of their other work (1890 cycles per pair of
-// tiles measured; the products need 1280: 48 cycles per K = 16 step of S at
-// N = 64, where shared memory is the limit, and 64 of P V).  Measured and left,
-// 16,384 tokens, window 4096, 32 q / 4 KV heads, 890 us as here (1000 us when
-// repeated until the power limit lowers the clock): one CTA with two row tiles on
-// shared key tiles (1056 us: the two run in step, and their exponentials
-// collide), key tiles of 128 in that form (1120 us), a quarter of the
-// exponentials as a polynomial (915 us), two warps per row with the maximum
-// agreed between them (1005 us).
+// No single unit is full: per 64 scores of two rows a scheduler has 1024 cycles
+// of exponentials (16 a clock and SM), and the two warps that share it overlap
+// them with only part of their other work (1890 cycles per pair of tiles
+// measured: exponentials 60% busy, the tensor core 59%, issue 53%); a division
+// of the work that overlaps more of it has not been found among those below (the
+// products need 1280: 48 cycles per K = 16 step of S at N = 64, where shared
+// memory is the limit, and 64 of P V).  16,384 tokens, window 4096, 32 q / 4 KV
+// heads: 860 us (980 us when repeated until the power limit lowers the clock).
+// Measured and left, against 890 us then: one CTA with two row tiles on shared
+// key tiles (1056 us: the two run in step, and their exponentials collide), key
+// tiles of 128 in that form (1120 us), a quarter of the exponentials as a
+// polynomial (915 us), two warps per row with the maximum agreed between them
+// (1005 us).
 // A narrow window is bound by what an item costs beside its tiles: 65,536
-// tokens, window 128, 16,384 items of three tiles: 380 us (443 while the 128
-// registers a thread may have did not suffice and 28 bytes were spilled; the
+// tokens, window 128, 16,384 items of three tiles: 365 to 385 us (443 while the
+// 128 registers a thread may have did not suffice and 28 bytes were spilled; the
 // outputs' way to memory was 120 us of that).  Measured and left there: no
 // exponentials for 32 columns that no row of a warp sees (5% slower: spills),
 // stores of each softmax warp's own rows, 32 dims at a time, without warp 7
@@ -54,9 +56,11 @@
 // past the last token (the copies fill what lies past the sinks with zeros).  Warp 7
 // looks through those before their product and sets what is not finite there to
 // zero; where it found some, each row adds those that it does see (whatever
-// their weights, they make the sum non-finite) to its outputs at the end.  What
-// this costs depends on T alone, however many values there are and however long
-// the prompt is.
+// their weights, they make the sum non-finite) to its outputs at the end.  The
+// look is hidden behind the softmax (380 us for the narrow window with it, 385
+// before); an item that has to give values back pays for T alone, however long
+// the prompt is: with such values in every key the narrow window takes 1.4 ms
+// (0.33 without, both in single calls) and the wide one 1.07 (0.86).
 // Every mbarrier wait is bounded, as in attention.cuh.
 #pragma once
 

@@ -414,10 +414,13 @@ RBS_API rbs_status rope_qk_norm(const rbs_bf16_tensor* q_in, rbs_bf16_tensor* q_
  * in bf16 tensor-core products with fp32 accumulation and softmax.
  *   Q         [B, Lq, Hq, 128] bf16; K, V [B, Lk, Hkv, 128] bf16; each with stride_h <= stride_s; Hq / Hkv <= 128;
  *             any lengths and q_offset >= 0 (keys past Lk do not exist)
- *   softmax_scale  <= 0 selects 1/sqrt(128)
+ *   softmax_scale  <= 0 selects 1/sqrt(128); scale q_t.k_s has to stay below 2^29 in size (fp32 does not tell such
+ *             scores apart)
  *   O         out [B, Lq, Hq, 128] bf16 (may not alias Q, K or V)
  *   lse       optional out [B, Hq, Lq] fp32 = ln sum_s exp(scale q_t.k_s) (-inf where no key is seen, O = 0)
- * Keys and values that a query does not see do not reach it, NaN and infinities included.  Uses no workspace. */
+ * Keys and values that a query does not see do not reach it, NaN and infinities included; a NaN or an infinity that it
+ * does see makes its output in that dim NaN or infinite.  Such values cost time only in keys at the window's edges, and
+ * that does not grow with the lengths.  Uses no workspace. */
 RBS_API rbs_status swa_prefill(const rbs_bf16_tensor* Q, const rbs_bf16_tensor* K, const rbs_bf16_tensor* V,
                                int32_t window, int32_t sinks, int64_t q_offset, float softmax_scale,
                                rbs_bf16_tensor* O, float* lse, rbs_stream_t stream);
@@ -499,7 +502,7 @@ RBS_API rbs_status kv4_load(const rbs_kv4_cache* cache, const int32_t* slots, rb
  *   lens         [B] int32, tokens held including the new ones; out of [0, max_pages * page_size] is brought into
  *                range with RBS_DEVERR_LENGTH
  *   starts       [B] int32 or NULL
- *   softmax_scale  <= 0 selects 1/sqrt(128)
+ *   softmax_scale  <= 0 selects 1/sqrt(128); any scores that fp32 holds
  *   workspace    rbs_kv4_attend_workspace_bytes(...) bytes, 16-byte aligned, needs no initialisation; calls that
  *                may overlap on the GPU need one each
  *   O            out [B, Lq, Hq, 128] bf16 (may not alias Q)
